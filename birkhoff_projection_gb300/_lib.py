@@ -64,6 +64,46 @@ SIGNATURES = {
     "birkhoff4_mufu_probe": (_int, [ctypes.POINTER(ctypes.c_float), _int, _int, _vp]),
 }
 
+# The functions of hc_block.h and adamw.h.
+BLOCK_SIGNATURES = {
+    "hcb_workspace_bytes": (ctypes.c_size_t, [_i64, ctypes.c_int32, ctypes.c_int32]),
+    "hcb_enter": (_int, [_vp, _vp]),
+    "hcb_enter_backward": (_int, [_vp, _vp]),
+    "hcb_leave": (_int, [_vp, _vp]),
+    "hcb_leave_backward": (_int, [_vp, _vp]),
+    "adamw_step": (_int, [_vp, ctypes.c_int32, _vp, _vp]),
+}
+
+HCB_MAX_STREAMS, HCB_MAX_CHANNELS = 8, 16384
+HCB_ACT_NONE, HCB_ACT_SIGMOID, HCB_ACT_SILU, HCB_ACT_LINEAR = 0, 1, 2, 3
+ADAMW_BLOCK = 128
+
+
+def _fields(kind, names):
+    return [(n, kind) for n in names.split()]
+
+
+class HcbArgs(ctypes.Structure):
+    """hcb_args."""
+    _fields_ = (
+        _fields(_i64, "T") + _fields(ctypes.c_int32, "S C x_dtype y_dtype w_dtype wn_dtype p_dtype a_dtype b_dtype act norm")
+        + _fields(ctypes.c_float, "eps eps_next scale")
+        + _fields(_vp, "x y gate P a b w w_next dout dh dres out_in")
+        + _fields(_i64, "x_ts x_ss y_ts gate_ts P_ts a_ts b_ts dout_ts dout_ss dh_ts dres_ts dres_ss out_ts out_ss")
+        + _fields(_vp, "h out dx dy dgate dP da db dw dw_next workspace")
+        + _fields(ctypes.c_size_t, "workspace_bytes"))
+
+
+class AdamwTensor(ctypes.Structure):
+    """adamw_tensor."""
+    _fields_ = _fields(_vp, "p g m v m_scale v_scale master") + _fields(_i64, "n")
+
+
+class AdamwOpts(ctypes.Structure):
+    """adamw_opts."""
+    _fields_ = (_fields(ctypes.c_int32, "p_dtype g_dtype state_bits") + _fields(ctypes.c_double, "lr beta1 beta2 eps weight_decay")
+                + _fields(_i64, "step") + _fields(_vp, "grad_scale"))
+
 
 class Opts(ctypes.Structure):
     """birkhoff4_opts."""
@@ -92,7 +132,7 @@ def lib():
         if not os.path.exists(path):
             raise Birkhoff4Error("libbirkhoff4.so was not built")
         handle = ctypes.CDLL(path)
-        for name, (res, args) in SIGNATURES.items():
+        for name, (res, args) in {**SIGNATURES, **BLOCK_SIGNATURES}.items():
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args
