@@ -163,8 +163,8 @@ __device__ __forceinline__ float encode(float (&x)[kVec], bool root) {
   }
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  // 448 / most overflows below 2^-119; such a block's values count as zeros' neighbours
-  const float inv = most > 0.0f ? fminf(__fdiv_rn(kTop, most), 3.0e38f) : 0.0f;
+  // below about 2^-119 the factor would overflow: held at 3e38, it stores such a block's values smaller
+  const float inv = most > 0.0f ? fminf(__fmul_rn(kTop, __frcp_rn(most)), 3.0e38f) : 0.0f;
 #pragma unroll
   for (int k = 0; k < kVec; ++k) {
     float q = __fmul_rn(x[k], inv);
@@ -172,7 +172,7 @@ __device__ __forceinline__ float encode(float (&x)[kVec], bool root) {
     if (!(fabsf(x[k]) < INFINITY)) q = NAN;
     x[k] = q;
   }
-  return __fdiv_rn(most, kTop);
+  return __fmul_rn(most, 1.0f / kTop);
 }
 
 template <class TP, class TG, bool MASTER, bool EIGHT>

@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(512) finish_weights_kernel(const Finish f) {
   const float* part = f.part[which];
   float d = 0.0f;
   if (c < f.C)
-    for (int r = threadIdx.y; r < f.rows; r += 16) d += part[int64_t(r) * f.C + c];
+    for (int r = threadIdx.y; r < f.rows; r += 16) d += part[int64_t(r) * pitch(f.C) + c];
   s[threadIdx.y][threadIdx.x] = d;
   __syncthreads();
   if (threadIdx.y != 0 || c >= f.C) return;
@@ -115,7 +115,7 @@ int place_workspace(const hcb_args* a, Params* p) {
       a->workspace_bytes < hcb_workspace_bytes(a->T, a->C, n))
     return B4_EINVAL;
   float* w = static_cast<float*>(a->workspace);
-  const int64_t row = std::min<int64_t>(a->T, kMaxRows) * a->C;
+  const int64_t row = std::min<int64_t>(a->T, kMaxRows) * pitch(a->C);
   if (a->dw != nullptr) p->dw = w, w += row;
   if (n == 2 || a->dw == nullptr) p->dwn = w;
   return B4_OK;
@@ -143,7 +143,7 @@ extern "C" {
 
 size_t hcb_workspace_bytes(int64_t T, int32_t C, int32_t weights) {
   if (T <= 0 || C < 1 || C > HCB_MAX_CHANNELS || weights < 1 || weights > 2) return 0;
-  return static_cast<size_t>(std::min<int64_t>(T, kMaxRows)) * C * weights * sizeof(float);
+  return static_cast<size_t>(std::min<int64_t>(T, kMaxRows)) * pitch(C) * weights * sizeof(float);
 }
 
 int hcb_enter(const hcb_args* a, birkhoff4_stream_t stream) {

@@ -1,15 +1,28 @@
 // hcb_common.cuh -- pieces shared by the hyper-connection block kernels
-// (hcb_enter.cu, hcb_leave.cu, hcb_leave_bwd.cu): row vectors in fp32 and
-// bf16, the sums over a row, gates, and the launch shape.
+// (hcb_enter.cu, hcb_leave.cu, hcb_leave_bwd.cu): rows that travel through
+// shared memory ahead of their use, the sums over a row, gates, and the
+// launch shape.
 //
 // Mapping.  A group of G threads (a power of two, a warp at least) takes one
 // token at a time; a CTA holds NG groups, and the grid is persistent (SMs x
-// resident CTAs), so that a thread meets the same channels in every token
-// and can keep its share of the weight gradients in shared memory until its
-// last token.  Thread l of a group owns the channels [(k G + l) V, + V) for
-// k = 0, 1, ...; what a row's second pass needs again is kept in fp32 in
-// shared memory by the thread that wrote it (no barrier), while the barriers
-// of the sums are between the threads of one group only.
+// resident CTAs).  Thread l of a group owns the channels [(k G + l) V, + V)
+// of every token, k = 0 .. K - 1, where V elements are 16 bytes of the wider
+// row type.
+//
+// Loads.  All of these kernels are bound by memory, and a row's sums keep a
+// group waiting at a barrier; loads into registers then left the memory idle
+// (40% of its rate).  So a thread copies its own vectors of the rows that it
+// will need next (cp.async) into its own slots of shared memory, DEPTH items
+// ahead of its work and across the end of a token: bytes in flight cost no
+// registers, and since only the thread that copied a slot reads it, the ring
+// needs no barrier and no wait other than the thread's own copies.  That asks
+// of every layout of a slot that a byte belongs to the same thread in all
+// kinds of items that pass through it.
+//
+// What a row's second pass needs again is kept in shared memory the same
+// way, by the thread that will read it; so are a thread's shares of the
+// weight gradients, which it holds until its last token.  All of it lies
+// [.. ][thread], so that a warp's accesses are conflict-free.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -35,85 +48,247 @@ constexpr int kMaxGroup = 512;  // threads of a group at most
 constexpr int kMaxRows = 640;   // CTAs of a backward pass at most (rows of partial weight gradients)
 
 // ---------------------------------------------------------------------------
-// V consecutive elements of a row as floats
+// V consecutive elements of a row, and their way through shared memory.
+//
+// ODD rows need not lie on 16-byte boundaries (any alignment of the element
+// type): they are copied in 4-byte words, of which a bf16 row that begins in
+// the middle of a word takes one more, and end with C wherever that is
+// (`left` elements from here).  The word around a row's first element is read
+// whole; no allocation begins inside a word.  Past the row's last element
+// nothing is read (the copy's source size) and the slot holds zeros.
 // ---------------------------------------------------------------------------
-template <class T, int V>
-struct Row;
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
-template <int V>
-struct Row<float, V> {
-  static_assert(V == 1 || V == 4, "");
-  __device__ __forceinline__ static void load(const float* p, float (&v)[V]) {
-    if constexpr (V == 4) {
-      const float4 q = *reinterpret_cast<const float4*>(p);
-      v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-    } else {
-      v[0] = *p;
-    }
-  }
-  __device__ __forceinline__ static void store(float* p, const float (&v)[V]) {
-    if constexpr (V == 4) {
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-      *p = v[0];
-    }
-  }
-  __device__ __forceinline__ static float round(float x) { return x; }
-};
+template <class T, int V, bool ODD>
+struct Row {
+  static constexpr int BYTES = V * static_cast<int>(sizeof(T));
+  static constexpr int WORDS = BYTES / 4 + (ODD && sizeof(T) == 2 ? 1 : 0);
+  static constexpr int SLOT = 4 * WORDS;  // bytes of a thread's slot
+  static_assert(BYTES == 16 || BYTES == 8, "");
 
-template <int V>
-struct Row<bf16_t, V> {
-  static_assert(V == 1 || V == 4 || V == 8, "");
-  __device__ __forceinline__ static void load(const bf16_t* p, float (&v)[V]) {
-    if constexpr (V == 8) {
-      const uint4 q = *reinterpret_cast<const uint4*>(p);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  // Begin the copy of p[0, V) into the slot of thread l in `s` (G slots).
+  __device__ __forceinline__ static void copy(char* s, int G, int l, const T* p, int left) {
+    if constexpr (!ODD) {
+      const uint32_t d = b4::smem_addr(s + l * BYTES);
+      if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(p) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(p) : "memory");
+    } else {
+      const int before = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 3);  // 0, or 2 for bf16
+      const char* q = reinterpret_cast<const char*>(p) - before;
+      const int end = before + min(left, V) * static_cast<int>(sizeof(T));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[2 * i] = b4::bf16lo(w[i]), v[2 * i + 1] = b4::bf16hi(w[i]);
-    } else if constexpr (V == 4) {
-      const uint2 q = *reinterpret_cast<const uint2*>(p);
-      v[0] = b4::bf16lo(q.x), v[1] = b4::bf16hi(q.x), v[2] = b4::bf16lo(q.y), v[3] = b4::bf16hi(q.y);
-    } else {
-      v[0] = b4::bf16lo(p->bits);
+      for (int w = 0; w < WORDS; ++w) {
+        const int n = max(0, min(4, end - 4 * w));
+        const char* src = n > 0 ? q + 4 * w : q;  // in bounds even where nothing is read
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                         b4::smem_addr(s + (w * G + l) * 4)),
+                     "l"(src), "r"(n)
+                     : "memory");
+      }
     }
   }
-  __device__ __forceinline__ static void store(bf16_t* p, const float (&v)[V]) {
-    if constexpr (V == 8) {
-      *reinterpret_cast<uint4*>(p) = make_uint4(b4::pack_bf16(v[0], v[1]), b4::pack_bf16(v[2], v[3]),
-                                                b4::pack_bf16(v[4], v[5]), b4::pack_bf16(v[6], v[7]));
-    } else if constexpr (V == 4) {
-      *reinterpret_cast<uint2*>(p) = make_uint2(b4::pack_bf16(v[0], v[1]), b4::pack_bf16(v[2], v[3]));
+  __device__ __forceinline__ static void unpack(const uint32_t (&w)[BYTES / 4], float (&v)[V]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = __uint_as_float(w[i]);
     } else {
-      p->bits = static_cast<uint16_t>(b4::pack_bf16(v[0], 0.0f));
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) v[2 * i] = b4::bf16lo(w[i]), v[2 * i + 1] = b4::bf16hi(w[i]);
+    }
+  }
+  // The arrived slot's elements (p: where they came from, for its alignment).
+  __device__ __forceinline__ static void arrived(const char* s, int G, int l, const T* p, float (&v)[V]) {
+    uint32_t w[BYTES / 4];
+    if constexpr (!ODD) {
+      if constexpr (BYTES == 16) {
+        const uint4 q = *reinterpret_cast<const uint4*>(s + l * BYTES);
+        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+      } else {
+        const uint2 q = *reinterpret_cast<const uint2*>(s + l * BYTES);
+        w[0] = q.x, w[1] = q.y;
+      }
+    } else {
+      uint32_t raw[WORDS];
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) raw[i] = *reinterpret_cast<const uint32_t*>(s + (i * G + l) * 4);
+      if constexpr (sizeof(T) == 2) {
+        const uint32_t shift = (reinterpret_cast<uintptr_t>(p) & 3) * 8;
+#pragma unroll
+        for (int i = 0; i < BYTES / 4; ++i) w[i] = __funnelshift_r(raw[i], raw[i + 1], shift);
+      } else {
+#pragma unroll
+        for (int i = 0; i < BYTES / 4; ++i) w[i] = raw[i];
+      }
+    }
+    unpack(w, v);
+  }
+  // p[0, min(V, left)) read directly, zeros behind.
+  __device__ __forceinline__ static void load(const T* p, float (&v)[V], int left) {
+    if constexpr (ODD) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        v[i] = 0.0f;
+        if (i < left) {
+          if constexpr (sizeof(T) == 4)
+            v[i] = p[i];
+          else
+            v[i] = b4::bf16lo(p[i].bits);
+        }
+      }
+    } else {
+      uint32_t w[BYTES / 4];
+#pragma unroll
+      for (int i = 0; i < BYTES / 8; ++i) {
+        const uint2 q = reinterpret_cast<const uint2*>(p)[i];
+        w[2 * i] = q.x, w[2 * i + 1] = q.y;
+      }
+      unpack(w, v);
+    }
+  }
+  // Round and write v to p[0, min(V, left)).
+  __device__ __forceinline__ static void store(T* p, const float (&v)[V], int left) {
+    uint32_t w[BYTES / 4];
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i] = __float_as_uint(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) w[i] = b4::pack_bf16(v[2 * i], v[2 * i + 1]);
+    }
+    if constexpr (!ODD) {
+      if constexpr (BYTES == 16)
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+      else
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < left) p[i] = v[i];
+    } else {
+      uint16_t* e = reinterpret_cast<uint16_t*>(p);
+      if (left < V) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (i < left) e[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+      } else if ((reinterpret_cast<uintptr_t>(p) & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+      } else {
+        e[0] = static_cast<uint16_t>(w[0]);
+#pragma unroll
+        for (int i = 0; i < V / 2 - 1; ++i)
+          reinterpret_cast<uint32_t*>(e + 1)[i] = __funnelshift_r(w[i], w[i + 1], 16);
+        e[V - 1] = static_cast<uint16_t>(w[V / 2 - 1] >> 16);
+      }
     }
   }
   __device__ __forceinline__ static float round(float x) {
+    if constexpr (sizeof(T) == 4) return x;
     return b4::bf16lo(b4::pack_bf16(x, 0.0f));
   }
 };
 
-// fp32 scratch of a row in shared memory (V floats at a multiple of V)
+// V floats that a thread keeps for itself: item k of K in `s` (K V G floats).
 template <int V>
-__device__ __forceinline__ void keep(float* s, const float (&v)[V]) {
-  if constexpr (V >= 4) {
+__device__ __forceinline__ void keep(float* s, int G, int l, int k, const float (&v)[V]) {
 #pragma unroll
-    for (int i = 0; i < V; i += 4)
-      *reinterpret_cast<float4*>(s + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-  } else {
-    s[0] = v[0];
-  }
+  for (int i = 0; i < V / 4; ++i)
+    reinterpret_cast<float4*>(s)[(k * (V / 4) + i) * G + l] =
+        make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
 template <int V>
-__device__ __forceinline__ void kept(const float* s, float (&v)[V]) {
-  if constexpr (V >= 4) {
+__device__ __forceinline__ void kept(const float* s, int G, int l, int k, float (&v)[V]) {
 #pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const float4 q = *reinterpret_cast<const float4*>(s + i);
-      v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
-    }
-  } else {
-    v[0] = s[0];
+  for (int i = 0; i < V / 4; ++i) {
+    const float4 q = reinterpret_cast<const float4*>(s)[(k * (V / 4) + i) * G + l];
+    v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
   }
+}
+// V elements of a row kept in the row's type (they came from it: exact).
+template <class T, int V>
+__device__ __forceinline__ void keep_row(char* s, int G, int l, int k, const float (&v)[V]) {
+  if constexpr (sizeof(T) == 4) {
+    keep<V>(reinterpret_cast<float*>(s), G, l, k, v);
+  } else if constexpr (V == 8) {
+    reinterpret_cast<uint4*>(s)[k * G + l] = make_uint4(b4::pack_bf16(v[0], v[1]), b4::pack_bf16(v[2], v[3]),
+                                                        b4::pack_bf16(v[4], v[5]), b4::pack_bf16(v[6], v[7]));
+  } else {
+    reinterpret_cast<uint2*>(s)[k * G + l] = make_uint2(b4::pack_bf16(v[0], v[1]), b4::pack_bf16(v[2], v[3]));
+  }
+}
+template <class T, int V>
+__device__ __forceinline__ void kept_row(const char* s, int G, int l, int k, float (&v)[V]) {
+  if constexpr (sizeof(T) == 4) {
+    kept<V>(reinterpret_cast<const float*>(s), G, l, k, v);
+  } else {
+    uint32_t w[V / 2];
+    if constexpr (V == 8) {
+      const uint4 q = reinterpret_cast<const uint4*>(s)[k * G + l];
+      w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    } else {
+      const uint2 q = reinterpret_cast<const uint2*>(s)[k * G + l];
+      w[0] = q.x, w[1] = q.y;
+    }
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) v[2 * i] = b4::bf16lo(w[i]), v[2 * i + 1] = b4::bf16hi(w[i]);
+  }
+}
+
+// A thread's shares of a weight gradient: in shared memory until the end, or,
+// where rows are too long for that, in the group's row of the partial sums
+// (global memory that only this thread touches; such groups are CTAs).
+template <int V>
+struct WeightShare {
+  float *s, *g;
+  __device__ __forceinline__ void zero(int G, int l, int K, int C) {
+    const float z[V] = {};
+    for (int k = 0; k < K; ++k) {
+      if (g == nullptr)
+        keep<V>(s, G, l, k, z);
+      else if ((k * G + l) * V < C)
+        put((k * G + l) * V, z);
+    }
+  }
+  __device__ __forceinline__ void add(int G, int l, int k, const float (&v)[V]) {
+    float d[V];
+    if (g == nullptr) {
+      kept<V>(s, G, l, k, d);
+    } else {
+      const float4* q = reinterpret_cast<const float4*>(g + (k * G + l) * V);
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        const float4 x = q[i];
+        d[4 * i] = x.x, d[4 * i + 1] = x.y, d[4 * i + 2] = x.z, d[4 * i + 3] = x.w;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) d[i] += v[i];
+    if (g == nullptr)
+      keep<V>(s, G, l, k, d);
+    else
+      put((k * G + l) * V, d);
+  }
+
+ private:
+  __device__ __forceinline__ void put(int c, const float (&v)[V]) {
+    float4* q = reinterpret_cast<float4*>(g + c);
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) q[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  }
+};
+
+// The float of channel c in what was kept.
+template <int V>
+__device__ __forceinline__ int kept_at(int G, int c) {
+  const int vec = c / V, k = vec / G, l = vec % G, e = c % V;
+  return ((k * (V / 4) + e / 4) * G + l) * 4 + e % 4;
 }
 
 // A pointer to fp32 or bf16 values, told apart at run time: coefficients and
@@ -124,21 +299,27 @@ struct Any {
   __device__ __forceinline__ float at(int64_t i) const {
     return bf16 ? b4::bf16lo(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
   }
-  template <int V>
-  __device__ __forceinline__ void load(int64_t i, float (&v)[V]) const {  // 1 where absent
+  // Elements [i, i + V), 1 where there are none (left: elements from i on).
+  template <int V, bool ODD>
+  __device__ __forceinline__ void load(int i, int left, float (&v)[V]) const {
     if (p == nullptr) {
 #pragma unroll
       for (int k = 0; k < V; ++k) v[k] = 1.0f;
-    } else if (bf16) {
-      Row<bf16_t, V>::load(static_cast<const bf16_t*>(p) + i, v);
-    } else if constexpr (V == 8) {
-      float lo[4], hi[4];
-      Row<float, 4>::load(static_cast<const float*>(p) + i, lo);
-      Row<float, 4>::load(static_cast<const float*>(p) + i + 4, hi);
+    } else if constexpr (ODD) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = lo[k], v[4 + k] = hi[k];
+      for (int k = 0; k < V; ++k) v[k] = k < left ? at(i + k) : 0.0f;
+    } else if (bf16) {
+#pragma unroll
+      for (int k = 0; k < V; k += 4) {
+        const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i + k);
+        v[k] = b4::bf16lo(q.x), v[k + 1] = b4::bf16hi(q.x), v[k + 2] = b4::bf16lo(q.y), v[k + 3] = b4::bf16hi(q.y);
+      }
     } else {
-      Row<float, V>::load(static_cast<const float*>(p) + i, v);
+#pragma unroll
+      for (int k = 0; k < V; k += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + k);
+        v[k] = q.x, v[k + 1] = q.y, v[k + 2] = q.z, v[k + 3] = q.w;
+      }
     }
   }
 };
@@ -156,7 +337,8 @@ __device__ __forceinline__ void put_any(void* p, int32_t bf16, int64_t i, float 
 struct Params {
   int64_t T;
   int32_t S, C;
-  int32_t G;  // threads of a group
+  int32_t G;            // threads of a group
+  int32_t group_bytes;  // shared memory of a group
   int32_t act, norm;
   float eps, eps_next, scale;
   const void *x, *y, *gate, *dout, *dh, *dres, *out_in;
@@ -164,7 +346,65 @@ struct Params {
   int64_t x_ts, x_ss, y_ts, gate_ts, P_ts, a_ts, b_ts, dout_ts, dout_ss, dh_ts, dres_ts, dres_ss,
       out_ts, out_ss;
   void *h, *out, *dx, *dy, *dgate, *dP, *da, *db;
-  float *dw, *dwn;  // partial weight gradients [CTAs, C]
+  float *dw, *dwn;  // partial weight gradients [CTAs, pitch(C)]
+  int32_t direct;   // rows too long to keep all of: the shares lie there from
+                    // the start, and y and dh are read a second time
+};
+
+// Floats of a row of partial weight gradients: whole vectors.
+__host__ __device__ constexpr int pitch(int C) { return (C + 7) / 8 * 8; }
+
+// Write a CTA's sums of its NG groups' shares (`step` floats apart) to its row.
+template <int V>
+__device__ __forceinline__ void sum_shares(const float* s, int step, int G, int NG, int C, float* row) {
+  for (int c = threadIdx.x; c < C; c += blockDim.x) {
+    const float* at = s + kept_at<V>(G, c);
+    float d = 0.0f;
+    for (int g = 0; g < NG; ++g) d += at[g * step];
+    row[c] = d;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// A token's coefficients, fetched one token ahead: lane l of every warp loads
+// value l (and l + 32, ...), and the warp spreads them through a few floats
+// of shared memory of its own.  Order: P [SP, SP], then b [SP], then a [SP];
+// streams that are not there have zeros, absent arrays ones.
+// ---------------------------------------------------------------------------
+template <int SP, bool P, bool B, bool A>
+struct Coefficients {
+  static constexpr int NP = P ? SP * SP : 0, NB = NP + (B ? SP : 0), N = NB + (A ? SP : 0);
+  static constexpr int CH = (N + 31) / 32;
+  static constexpr int FLOATS = (N + 3) / 4 * 4;
+  float next[CH];
+  __device__ __forceinline__ void fetch(const Params& p, int64_t t, int lane) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int n = c * 32 + lane;
+      float v = 0.0f;
+      if (n < NP) {
+        const int i = n / SP, j = n % SP;
+        if (p.P.p != nullptr && i < p.S && j < p.S) v = p.P.at(t * p.P_ts + i * p.S + j);
+      } else if (n < NB) {
+        if (n - NP < p.S) v = p.b.p != nullptr ? p.b.at(t * p.b_ts + n - NP) : 1.0f;
+      } else if (n < N) {
+        if (n - NB < p.S) v = p.a.p != nullptr ? p.a.at(t * p.a_ts + n - NB) : 1.0f;
+      }
+      next[c] = v;
+    }
+  }
+  // Put the fetched values where the warp reads them.
+  __device__ __forceinline__ void spread(float* s, int lane) const {
+    __syncwarp();  // the last token's readers are done
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (c * 32 + lane < FLOATS) s[c * 32 + lane] = next[c];
+    __syncwarp();
+  }
+  __device__ __forceinline__ static void read(const float* s, int from, float (&v)[SP]) {
+#pragma unroll
+    for (int i = 0; i < SP; ++i) v[i] = s[from + i];
+  }
 };
 
 // ---------------------------------------------------------------------------
@@ -281,13 +521,14 @@ __device__ __forceinline__ void gate_of(int act, float g, float& value, float& s
 // ---------------------------------------------------------------------------
 // Launch shape
 // ---------------------------------------------------------------------------
+constexpr size_t kSmemMax = 232448;  // shared memory of a CTA
+
 struct Shape {
   int G, NG;
 };
 
 int sms();  // SMs of the current device (hcb_api.cu)
 
-inline int padded(int C) { return (C + 3) / 4 * 4; }  // floats of a kept row
 
 // Threads of a group: two vectors of a row to a thread where the tokens fill
 // the GPU, one where they do not (a longer group shortens a token's path).
@@ -298,6 +539,7 @@ inline Shape shape_of(int64_t T, int C, int V, int max_group) {
   while (G < max_group && G * per < vecs) G *= 2;
   return {G, std::max(1, kThreads / G)};
 }
+inline int items(int C, int V, int G) { return (C + V * G - 1) / (V * G); }  // K
 
 // Resident CTAs per SM of a kernel at (threads, shared bytes), remembered per
 // kernel for the last such pair: the occupancy query is a host call that
@@ -321,7 +563,7 @@ cudaError_t resident(int threads, size_t smem, int* out) {
   e = cudaFuncGetAttributes(&fa, KERN);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           232448 - static_cast<int>(fa.sharedSizeBytes));
+                           static_cast<int>(kSmemMax) - static_cast<int>(fa.sharedSizeBytes));
   if (e != cudaSuccess) return e;
   int occ = 0;
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, KERN, threads, smem);
@@ -331,11 +573,25 @@ cudaError_t resident(int threads, size_t smem, int* out) {
   return cudaSuccess;
 }
 
-// Persistent launch of KERN: NG tokens to a CTA, `smem` bytes for each token's
-// group.  At most max_grid CTAs; the grid is returned in *grid.
+// The shape whose groups need bytes(G, direct), shrunk until it fits; direct
+// (Params) where no group of 128 threads does otherwise.
+template <class B>
+Shape fitted(Shape sh, bool may_direct, int* direct, B&& bytes) {
+  *direct = 0;
+  while (bytes(sh.G, false) * sh.NG > kSmemMax && sh.NG > 1) sh.NG /= 2;
+  while (bytes(sh.G, false) > kSmemMax && (sh.G > 128 || (!may_direct && sh.G > 32))) sh.G /= 2;
+  if (bytes(sh.G, false) > kSmemMax && may_direct) {
+    *direct = 1, sh.NG = 1;
+    while (bytes(sh.G, true) > kSmemMax && sh.G > 32) sh.G /= 2;
+  }
+  return sh;
+}
+
+// Persistent launch of KERN: NG groups to a CTA, smem_group bytes to a group.  At most max_grid CTAs; the grid is returned in *grid.
 template <auto KERN>
 cudaError_t launch(Params p, Shape sh, size_t smem_group, int max_grid, int* grid, cudaStream_t s) {
-  p.G = sh.G;
+  smem_group = (smem_group + 15) / 16 * 16;
+  p.G = sh.G, p.group_bytes = static_cast<int32_t>(smem_group);
   const size_t smem = smem_group * sh.NG;
   int occ = 0;
   const cudaError_t e = resident<KERN>(sh.G * sh.NG, smem, &occ);
@@ -346,16 +602,16 @@ cudaError_t launch(Params p, Shape sh, size_t smem_group, int max_grid, int* gri
   return cudaGetLastError();
 }
 
-// Call F.operator()<SP, TX, TY, V>() for the streams (rounded up to 1, 2, 4
-// or 8; the missing ones count as zeros), the row types and the vector width:
-// 16 bytes of the wider row type (8 bytes of bf16 at 8 streams, for the
-// registers), or single elements where rows do not allow vectors.
+// Call F.operator()<SP, TX, TY, V, ODD>() for the streams (rounded up to 1,
+// 2, 4 or 8; the missing ones count as zeros), the row types and alignment.
+// V elements are 16 bytes of the wider row type (8 bytes of bf16 at 8
+// streams, for the registers).
 template <int SP, class F>
 cudaError_t by_type(int x_bf16, int y_bf16, bool vec, F&& f) {
   constexpr int VB = SP == 8 ? 4 : 8;
-  if (x_bf16) return vec ? f.template operator()<SP, bf16_t, bf16_t, VB>() : f.template operator()<SP, bf16_t, bf16_t, 1>();
-  if (y_bf16) return vec ? f.template operator()<SP, float, bf16_t, 4>() : f.template operator()<SP, float, bf16_t, 1>();
-  return vec ? f.template operator()<SP, float, float, 4>() : f.template operator()<SP, float, float, 1>();
+  if (x_bf16) return vec ? f.template operator()<SP, bf16_t, bf16_t, VB, false>() : f.template operator()<SP, bf16_t, bf16_t, VB, true>();
+  if (y_bf16) return vec ? f.template operator()<SP, float, bf16_t, 4, false>() : f.template operator()<SP, float, bf16_t, 4, true>();
+  return vec ? f.template operator()<SP, float, float, 4, false>() : f.template operator()<SP, float, float, 4, true>();
 }
 template <class F>
 cudaError_t by_streams(int S, int x_bf16, int y_bf16, bool vec, F&& f) {

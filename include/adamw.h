@@ -18,9 +18,9 @@
  * Moments are fp32 (state_bits 32), or e4m3 numbers with one fp32 scale for
  * ADAMW_BLOCK consecutive elements (state_bits 8): the first moment m, and
  * the root sqrt(v) of the second, which has half of v's range of exponents.
- * A block's scale is the largest finite magnitude in it over 448 (e4m3's
- * largest number), and a code is the nearest e4m3 number to value * (448 /
- * largest), ties to even.  sqrt(v) > 0 never becomes 0: it is at least e4m3's
+ * A block's scale is the largest finite magnitude in it times the fp32 number
+ * 1/448 (448 is e4m3's largest), and a code is the nearest e4m3 number to
+ * value * (448 * (1 / largest)), ties to even, every operation rounded.  sqrt(v) > 0 never becomes 0: it is at least e4m3's
  * smallest number, so that a denominator does not vanish under a first
  * moment that is kept.  A value that is not finite is stored as e4m3's NaN
  * and leaves the others of its block alone.

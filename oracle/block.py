@@ -150,13 +150,13 @@ def encode(x, root):
     mag = np.where(np.isfinite(blocks), np.abs(blocks), np.float32(0))
     most = mag.max(1)
     with np.errstate(divide="ignore", over="ignore", invalid="ignore"):
-        inv = np.where(most > 0, np.minimum(np.float32(TOP) / most, np.float32(3.0e38)), np.float32(0)).astype(np.float32)
+        inv = np.where(most > 0, np.minimum(np.float32(TOP) * (np.float32(1) / most), np.float32(3.0e38)), np.float32(0)).astype(np.float32)
         q = blocks * inv[:, None]
         if root:
             q = np.where(blocks > 0, np.maximum(q, np.float32(LEAST)), q)
         q = np.where(np.isfinite(blocks), q, np.float32(np.nan))
     code = np.minimum(np.maximum(e4m3(q), -TOP), TOP)
-    return code.reshape(-1)[:n], most / np.float32(TOP)
+    return code.reshape(-1)[:n], most * (np.float32(1) / np.float32(TOP))
 
 
 def decode(code, scale):
