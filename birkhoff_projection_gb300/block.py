@@ -17,18 +17,17 @@ or bf16 each.  Arithmetic is fp32, every result is rounded once.
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 from collections import namedtuple
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _DT, _on_device, _ptr, _stream
-from ._lib import (HCB_ACT_LINEAR, HCB_ACT_NONE, HCB_ACT_SIGMOID, HCB_ACT_SILU, HCB_MAX_CHANNELS, HCB_MAX_STREAMS,
-                   HcbArgs, check, lib)
+from . import _DT, _lib
+from ._lib import HCB_ACT_LINEAR, HCB_ACT_SIGMOID, HCB_ACT_SILU, HCB_MAX_CHANNELS, HCB_MAX_STREAMS, check
 
 __all__ = ["enter", "enter_backward", "leave", "leave_backward", "leave_enter", "leave_enter_backward",
-           "EnterGrads", "LeaveGrads", "LeaveEnterGrads"]
+           "workspace_bytes", "EnterGrads", "LeaveGrads", "LeaveEnterGrads"]
 
 _ACT = {"sigmoid": HCB_ACT_SIGMOID, "silu": HCB_ACT_SILU, "linear": HCB_ACT_LINEAR}
 
@@ -36,16 +35,42 @@ EnterGrads = namedtuple("EnterGrads", "dx da dweight")
 LeaveGrads = namedtuple("LeaveGrads", "dx dy dP db dgate dweight")
 LeaveEnterGrads = namedtuple("LeaveEnterGrads", "dx dy dP db dgate dweight da_next dweight_next")
 
+# hcb_args packed in one call (a ctypes structure filled field by field takes
+# longer than the smallest kernels): T; S C, seven types, act, norm; eps
+# eps_next scale; x y gate P a b w w_next dout dh dres out_in; their strides;
+# h out dx dy dgate dP da db dw dw_next workspace, workspace_bytes
+_ARGS = struct.Struct("<q11i3f12Q14q11QQ")
+_NONE = (None, 0, 0, 0)  # a tensor that is not there: itself, address, type, stride
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_functions = {}
 
-def _need(t, name, like=None):
+
+def _call(name, dev, args):
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(_lib.lib(), name)
+    if dev == torch.cuda.current_device():
+        status = f(args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = f(args, _raw_stream(dev))
+    if status:
+        check(status, name)
+
+
+def _wrong(t, name, shape, dtype, dev):
+    """Say what is wrong with a tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.dtype not in _DT:
         raise TypeError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if like is not None and t.device != like.device:
-        raise ValueError("%s must be on %s, got %s" % (name, like.device, t.device))
+    if dev is not None and t.get_device() != dev:
+        raise ValueError("%s must be on cuda:%d, got %s" % (name, dev, t.device))
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
 
 
 def _flat(t, inner):
@@ -53,133 +78,124 @@ def _flat(t, inner):
     it), the last dimension contiguous."""
     if t.dim() != inner + 1:
         t = t.flatten(0, t.dim() - inner - 1) if t.dim() > inner else t.unsqueeze(0)
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
         t = t.contiguous()
     return t
 
 
-class _Call:
-    """The arguments of one call: an hcb_args, and the tensors it points to."""
+def _x(x):
+    """(shape, leading shape, T, S, C, device) of the streams."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in _DT or not x.is_cuda:
+        _wrong(x, "x", None, None, None)
+    shape = x.shape
+    if len(shape) < 2:
+        raise ValueError("x must have shape [..., streams, channels], got %s" % (tuple(shape),))
+    S, C = shape[-2], shape[-1]
+    if not (1 <= S <= HCB_MAX_STREAMS and 1 <= C <= HCB_MAX_CHANNELS):
+        raise ValueError("x must have 1 to %d streams and 1 to %d channels, got %s"
+                         % (HCB_MAX_STREAMS, HCB_MAX_CHANNELS, tuple(shape)))
+    return shape, shape[:-2], x.numel() // (S * C), S, C, x.get_device()
 
-    def __init__(self, x):
-        _need(x, "x")
-        if x.dim() < 2:
-            raise ValueError("x must have shape [..., streams, channels], got %s" % (tuple(x.shape),))
-        self.lead, (self.S, self.C) = x.shape[:-2], x.shape[-2:]
-        if not (1 <= self.S <= HCB_MAX_STREAMS and 1 <= self.C <= HCB_MAX_CHANNELS):
-            raise ValueError("x must have 1 to %d streams and 1 to %d channels, got %s"
-                             % (HCB_MAX_STREAMS, HCB_MAX_CHANNELS, tuple(x.shape)))
-        self.x, self.device, self.keep = x, x.device, []
-        self.T = x.numel() // (self.S * self.C)
-        self.args = HcbArgs(T=self.T, S=self.S, C=self.C, x_dtype=_DT[x.dtype], norm=1)
 
-    def streams(self, t, name, field, ts, ss):
-        if t is not self.x:
-            _need(t, name, self.x)
-            if t.shape != self.x.shape or t.dtype != self.x.dtype:
-                raise ValueError("%s must have x's shape and dtype" % name)
-        t = _flat(t, 2)
-        self.keep.append(t)
-        a = self.args
-        setattr(a, field, t.data_ptr())
-        setattr(a, ts, t.stride(0))
-        setattr(a, ss, t.stride(1))
+def _streams(t, name, shape, dtype, dev):
+    """(tensor, address, token stride, stream stride) of x or what is shaped like it."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        _wrong(t, name, shape, dtype, dev)
+    if t.is_contiguous():
+        return t, t.data_ptr(), shape[-2] * shape[-1], shape[-1]
+    t = _flat(t, 2)
+    return t, t.data_ptr(), t.stride(0), t.stride(1)
 
-    def row(self, t, name, field, ts, dtype=None):
-        """A row of C channels per token, of y's type."""
-        _need(t, name, self.x)
-        if t.shape[:-1] != self.lead or t.shape[-1] != self.C:
-            raise ValueError("%s must have shape %s, got %s" % (name, (*self.lead, self.C), tuple(t.shape)))
-        if dtype is not None and t.dtype != dtype:
-            raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-        t = _flat(t, 1)
-        self.keep.append(t)
-        setattr(self.args, field, t.data_ptr())
-        setattr(self.args, ts, t.stride(0))
 
-    def y_type(self, dtype, name):
-        if dtype not in _DT:
-            raise TypeError("%s must be float32 or bfloat16, got %s" % (name, dtype))
-        if dtype == torch.float32 and self.x.dtype == torch.bfloat16:
-            raise TypeError("%s must be bfloat16 where x is" % name)
-        self.args.y_dtype = _DT[dtype]
+def _row(t, name, shape, dtype, dev):
+    """(tensor, address, token stride) of a row of C channels to a token."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        _wrong(t, name, shape, dtype, dev)
+    if t.is_contiguous():
+        return t, t.data_ptr(), shape[-1]
+    t = _flat(t, 1)
+    return t, t.data_ptr(), t.stride(0)
 
-    def coefficients(self, t, name, field, kind, ts, shape):
-        if t is None:
-            return
-        _need(t, name, self.x)
-        if t.shape != (*self.lead, *shape):
-            raise ValueError("%s must have shape %s, got %s" % (name, (*self.lead, *shape), tuple(t.shape)))
-        t = _flat(t, len(shape))
-        if len(shape) == 2 and t.stride(1) != shape[1]:
-            t = t.contiguous()
-        self.keep.append(t)
-        setattr(self.args, field, t.data_ptr())
-        setattr(self.args, kind, _DT[t.dtype])
-        setattr(self.args, ts, t.stride(0))
 
-    def weight(self, t, name, field, kind):
-        if t is None:
-            return
-        _need(t, name, self.x)
-        if t.shape != (self.C,):
-            raise ValueError("%s must have shape (%d,), got %s" % (name, self.C, tuple(t.shape)))
+def _few(t, name, shape, inner, dev):
+    """(tensor, address, type, token stride) of coefficients, or of a weight (inner 0)."""
+    if t is None:
+        return _NONE
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype not in _DT or t.get_device() != dev:
+        _wrong(t, name, shape, "float32 or bfloat16", dev)
+    kind = _DT[t.dtype]
+    if t.is_contiguous():
+        return t, t.data_ptr(), kind, 0 if inner == 0 else shape[-1] if inner == 1 else shape[-1] * shape[-1]
+    if inner == 0:
         t = t.contiguous()
-        self.keep.append(t)
-        setattr(self.args, field, t.data_ptr())
-        setattr(self.args, kind, _DT[t.dtype])
+        return t, t.data_ptr(), kind, 0
+    t = _flat(t, inner)
+    if inner == 2 and t.stride(1) != shape[-1]:
+        t = t.contiguous()
+    return t, t.data_ptr(), kind, t.stride(0)
 
-    def new(self, field, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        setattr(self.args, field, t.data_ptr())
-        return t
 
-    def like(self, field, t):
-        """A new tensor for the gradient of t (None where t is)."""
-        return None if t is None else self.new(field, t.shape, t.dtype)
+def _y_type(dtype, x, name):
+    kind = _DT.get(dtype)
+    if kind is None:
+        raise TypeError("%s must be float32 or bfloat16, got %s" % (name, dtype))
+    if kind == 0 and x.dtype == torch.bfloat16:
+        raise TypeError("%s must be bfloat16 where x is" % name)
+    return kind
 
-    def gated(self, gate, act, y):
-        if gate is None:
-            return
-        if act not in _ACT:
-            raise ValueError("act must be one of %s, got %r" % (", ".join(sorted(_ACT)), act))
-        self.args.act = _ACT[act]
-        self.row(gate, "gate", "gate", "gate_ts", y.dtype)
 
-    def scratch(self, workspace, weights):
-        need = lib().hcb_workspace_bytes(self.T, self.C, weights)
-        if need == 0:
-            return
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-        elif workspace.device != self.device or not workspace.is_contiguous() \
-                or workspace.numel() * workspace.element_size() < need:
-            raise ValueError("workspace needs %d bytes on %s" % (need, self.device))
-        self.keep.append(workspace)
-        self.args.workspace = workspace.data_ptr()
-        self.args.workspace_bytes = need
+def _gate(gate, act, shape, dtype, dev):
+    """(act, address, token stride, tensor) of the gate."""
+    if gate is None:
+        return 0, 0, 0, None
+    kind = _ACT.get(act)
+    if kind is None:
+        raise ValueError("act must be one of %s, got %r" % (", ".join(sorted(_ACT)), act))
+    t, ptr, ts = _row(gate, "gate", shape, dtype, dev)
+    return kind, ptr, ts, t
 
-    def run(self, name):
-        with _on_device(self.x):
-            check(getattr(lib(), name)(ctypes.byref(self.args), _stream(self.x)), name)
+
+def _like(t):
+    """A new contiguous tensor for the gradient of t, and its address."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("expected a torch.Tensor, got %s" % type(t).__name__)
+    g = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return g, g.data_ptr()
+
+
+def _scratch(workspace, T, C, weights, device):
+    need = workspace_bytes(T, C, weights) if weights else 0
+    if need == 0:
+        return None, 0, 0
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous() \
+            or workspace.numel() * workspace.element_size() < need:
+        raise ValueError("workspace needs %d bytes on %s" % (need, device))
+    return workspace, workspace.data_ptr(), need
 
 
 def workspace_bytes(tokens: int, channels: int, weights: int = 1) -> int:
     """Bytes of scratch of a backward pass with `weights` weight gradients
     (leave_enter_backward: up to 2)."""
-    return lib().hcb_workspace_bytes(tokens, channels, weights)
+    return _lib.lib().hcb_workspace_bytes(tokens, channels, weights)
 
 
 def _enter(x, a, weight, eps, out_dtype):
-    c = _Call(x)
+    shape, lead, T, S, C, dev = _x(x)
     dtype = out_dtype or x.dtype
-    c.y_type(dtype, "out_dtype")
-    c.args.eps = eps
-    c.streams(x, "x", "x", "x_ts", "x_ss")
-    c.coefficients(a, "a", "a", "a_dtype", "a_ts", (c.S,))
-    c.weight(weight, "weight", "w", "w_dtype")
-    h = c.new("h", (*c.lead, c.C), dtype)
-    c.run("hcb_enter")
+    yk = _y_type(dtype, x, "out_dtype")
+    x, xp, x_ts, x_ss = _streams(x, "x", shape, x.dtype, dev)
+    a, ap, ak, a_ts = _few(a, "a", shape[:-1], 1, dev)
+    weight, wp, wk, _ = _few(weight, "weight", shape[-1:], 0, dev)
+    h = torch.empty((*lead, C), dtype=dtype, device=x.device)
+    _call("hcb_enter", dev, _ARGS.pack(
+        T, S, C, _DT[x.dtype], yk, wk, 0, 0, ak, 0, 0, 1, eps, 0.0, 0.0,
+        xp, 0, 0, 0, ap, 0, wp, 0, 0, 0, 0, 0,
+        x_ts, x_ss, 0, 0, 0, a_ts, 0, 0, 0, 0, 0, 0, 0, 0,
+        h.data_ptr(), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0))
     return h
 
 
@@ -189,70 +205,96 @@ def enter_backward(dh: torch.Tensor, x: torch.Tensor, a: torch.Tensor = None, we
     a and weight are.  dres, shaped like x, is added to dx: the gradient that
     the streams have from elsewhere.  workspace: a uint8 tensor of
     workspace_bytes (allocated here if not given)."""
-    c = _Call(x)
-    _need(dh, "dh", x)
-    c.y_type(dh.dtype, "dh")
-    c.args.eps = eps
-    c.streams(x, "x", "x", "x_ts", "x_ss")
-    c.row(dh, "dh", "dh", "dh_ts")
-    c.coefficients(a, "a", "a", "a_dtype", "a_ts", (c.S,))
-    c.weight(weight, "weight", "w", "w_dtype")
+    shape, lead, T, S, C, dev = _x(x)
+    if not isinstance(dh, torch.Tensor):
+        _wrong(dh, "dh", None, None, None)
+    yk = _y_type(dh.dtype, x, "dh")
+    dh, hp, h_ts = _row(dh, "dh", torch.Size((*lead, C)), dh.dtype, dev)
+    rp = r_ts = r_ss = 0
     if dres is not None:
-        c.streams(dres, "dres", "dres", "dres_ts", "dres_ss")
-    got = EnterGrads(c.like("dx", x), c.like("da", a), c.like("dw", weight))
-    if weight is not None:
-        c.scratch(workspace, 1)
-    c.run("hcb_enter_backward")
-    return got
-
-
-def _leave_inputs(c, x, y, P, b, gate, act, weight, norm, scale, eps):
-    _need(y, "y", x)
-    c.y_type(y.dtype, "y")
-    c.args.norm, c.args.scale, c.args.eps = bool(norm), scale, eps
-    c.row(y, "y", "y", "y_ts")
-    c.gated(gate, act, y)
-    c.coefficients(P, "P", "P", "p_dtype", "P_ts", (c.S, c.S))
-    c.coefficients(b, "b", "b", "b_dtype", "b_ts", (c.S,))
-    c.weight(weight, "weight", "w", "w_dtype")
+        dres, rp, r_ts, r_ss = _streams(dres, "dres", shape, x.dtype, dev)
+    dx, dxp = _like(x)
+    da, dap = _like(a)
+    dw, dwp = _like(weight)
+    x, xp, x_ts, x_ss = _streams(x, "x", shape, x.dtype, dev)
+    a, ap, ak, a_ts = _few(a, "a", shape[:-1], 1, dev)
+    weight, wp, wk, _ = _few(weight, "weight", shape[-1:], 0, dev)
+    workspace, wsp, ws = _scratch(workspace, T, C, weight is not None, x.device)
+    _call("hcb_enter_backward", dev, _ARGS.pack(
+        T, S, C, _DT[x.dtype], yk, wk, 0, 0, ak, 0, 0, 1, eps, 0.0, 0.0,
+        xp, 0, 0, 0, ap, 0, wp, 0, 0, hp, rp, 0,
+        x_ts, x_ss, 0, 0, 0, a_ts, 0, 0, 0, h_ts, r_ts, r_ss, 0, 0,
+        0, 0, dxp, 0, 0, 0, dap, 0, dwp, 0, wsp, ws))
+    return EnterGrads(dx, da, dw)
 
 
 def _leave(x, y, P, b, gate, act, weight, norm, scale, eps, want_h, a_next, weight_next, eps_next):
-    c = _Call(x)
-    _leave_inputs(c, x, y, P, b, gate, act, weight, norm, scale, eps)
-    c.streams(x, "x", "x", "x_ts", "x_ss")
-    out = c.new("out", x.shape, x.dtype)
-    h = None
+    shape, lead, T, S, C, dev = _x(x)
+    if not isinstance(y, torch.Tensor):
+        _wrong(y, "y", None, None, None)
+    yt, row = y.dtype, torch.Size((*lead, C))
+    yk = _y_type(yt, x, "y")
+    y, yp, y_ts = _row(y, "y", row, yt, dev)
+    act, gp, g_ts, gate = _gate(gate, act, row, yt, dev)
+    x, xp, x_ts, x_ss = _streams(x, "x", shape, x.dtype, dev)
+    P, Pp, pk, P_ts = _few(P, "P", (*lead, S, S), 2, dev)
+    b, bp, bk, b_ts = _few(b, "b", shape[:-1], 1, dev)
+    weight, wp, wk, _ = _few(weight, "weight", shape[-1:], 0, dev)
+    out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    h, hp = None, 0
+    ap = ak = a_ts = wnp = wnk = 0
     if want_h:
-        c.args.eps_next = eps_next
-        c.coefficients(a_next, "a_next", "a", "a_dtype", "a_ts", (c.S,))
-        c.weight(weight_next, "weight_next", "w_next", "wn_dtype")
-        h = c.new("h", (*c.lead, c.C), y.dtype)
-    c.run("hcb_leave")
+        a_next, ap, ak, a_ts = _few(a_next, "a_next", shape[:-1], 1, dev)
+        weight_next, wnp, wnk, _ = _few(weight_next, "weight_next", shape[-1:], 0, dev)
+        h = torch.empty(row, dtype=yt, device=x.device)
+        hp = h.data_ptr()
+    _call("hcb_leave", dev, _ARGS.pack(
+        T, S, C, _DT[x.dtype], yk, wk, wnk, pk, ak, bk, act, bool(norm), eps, eps_next, scale,
+        xp, yp, gp, Pp, ap, bp, wp, wnp, 0, 0, 0, 0,
+        x_ts, x_ss, y_ts, g_ts, P_ts, a_ts, b_ts, 0, 0, 0, 0, 0, 0, 0,
+        hp, out.data_ptr(), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0))
     return out, h
 
 
 def _leave_backward(dout, dh, out, x, y, P, b, gate, act, weight, norm, scale, eps, a_next, weight_next, eps_next,
                     workspace):
-    c = _Call(x)
-    _leave_inputs(c, x, y, P, b, gate, act, weight, norm, scale, eps)
-    c.streams(dout, "dout", "dout", "dout_ts", "dout_ss")
-    if P is not None:
-        c.streams(x, "x", "x", "x_ts", "x_ss")
+    shape, lead, T, S, C, dev = _x(x)
+    if not isinstance(y, torch.Tensor):
+        _wrong(y, "y", None, None, None)
+    xt, yt, row = x.dtype, y.dtype, torch.Size((*lead, C))
+    yk = _y_type(yt, x, "y")
     # without a mixing matrix dx is dout, unless h's gradient is added to it
-    dx = c.new("dx", x.shape, x.dtype) if P is not None or dh is not None else dout
+    dx, dxp = _like(x) if P is not None or dh is not None else (dout, 0)
+    dy, dyp = _like(y)
+    dP, dPp = _like(P)
+    db, dbp = _like(b)
+    dgate, dgp = _like(gate)
+    dw, dwp = _like(weight)
+    dout, dop, do_ts, do_ss = _streams(dout, "dout", shape, xt, dev)
+    y, yp, y_ts = _row(y, "y", row, yt, dev)
+    act, gp, g_ts, gate = _gate(gate, act, row, yt, dev)
+    P, Pp, pk, P_ts = _few(P, "P", (*lead, S, S), 2, dev)
+    b, bp, bk, b_ts = _few(b, "b", shape[:-1], 1, dev)
+    weight, wp, wk, _ = _few(weight, "weight", shape[-1:], 0, dev)
+    xp = x_ts = x_ss = 0
+    if P is not None:
+        x, xp, x_ts, x_ss = _streams(x, "x", shape, xt, dev)
     da = dwn = None
+    hp = h_ts = op = o_ts = o_ss = ap = ak = a_ts = wnp = wnk = dap = dwnp = 0
     if dh is not None:
-        c.args.eps_next = eps_next
-        c.row(dh, "dh", "dh", "dh_ts", y.dtype)
-        c.streams(out, "out", "out_in", "out_ts", "out_ss")
-        c.coefficients(a_next, "a_next", "a", "a_dtype", "a_ts", (c.S,))
-        c.weight(weight_next, "weight_next", "w_next", "wn_dtype")
-        da, dwn = c.like("da", a_next), c.like("dw_next", weight_next)
-    got = (dx, c.like("dy", y), c.like("dP", P), c.like("db", b), c.like("dgate", gate), c.like("dw", weight))
-    c.scratch(workspace, (weight is not None) + (dwn is not None))
-    c.run("hcb_leave_backward")
-    return got, da, dwn
+        dh, hp, h_ts = _row(dh, "dh", row, yt, dev)
+        out, op, o_ts, o_ss = _streams(out, "out", shape, xt, dev)
+        da, dap = _like(a_next)
+        dwn, dwnp = _like(weight_next)
+        a_next, ap, ak, a_ts = _few(a_next, "a_next", shape[:-1], 1, dev)
+        weight_next, wnp, wnk, _ = _few(weight_next, "weight_next", shape[-1:], 0, dev)
+    workspace, wsp, ws = _scratch(workspace, T, C, (dw is not None) + (dwn is not None), x.device)
+    _call("hcb_leave_backward", dev, _ARGS.pack(
+        T, S, C, _DT[xt], yk, wk, wnk, pk, ak, bk, act, bool(norm), eps, eps_next, scale,
+        xp, yp, gp, Pp, ap, bp, wp, wnp, dop, hp, 0, op,
+        x_ts, x_ss, y_ts, g_ts, P_ts, a_ts, b_ts, do_ts, do_ss, h_ts, 0, 0, o_ts, o_ss,
+        0, 0, dxp, dyp, dgp, dPp, dap, dbp, dwp, dwnp, wsp, ws))
+    return (dx, dy, dP, db, dgate, dw), da, dwn
 
 
 def leave_backward(dout: torch.Tensor, x: torch.Tensor, y: torch.Tensor, P: torch.Tensor = None,
@@ -329,7 +371,12 @@ class _LeaveEnter(torch.autograd.Function):
 
 
 def _learns(*tensors):
-    return torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in tensors)
+    if not torch.is_grad_enabled():
+        return False
+    for t in tensors:
+        if t is not None and getattr(t, "requires_grad", False):
+            return True
+    return False
 
 
 def enter(x: torch.Tensor, a: torch.Tensor = None, weight: torch.Tensor = None, *, eps: float = 1e-6,

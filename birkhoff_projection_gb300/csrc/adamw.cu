@@ -28,23 +28,26 @@ using b4::bf16_t;
 constexpr int kThreads = 256;
 constexpr int kVec = 8;                    // elements of a thread at a time
 constexpr int kChunk = kThreads * kVec;    // elements of a CTA
-constexpr int kTable = 256;                // tensors of a launch
+constexpr int kTable = 256;                // tensors of a launch at most
 constexpr float kTop = 448.0f;             // e4m3's largest number
 constexpr float kLeast = 0.001953125f;     // its smallest positive one, 2^-9
 static_assert(ADAMW_BLOCK % kVec == 0 && kChunk % ADAMW_BLOCK == 0 && ADAMW_BLOCK / kVec == 16, "");
 
+struct Entry {
+  void* p;
+  const void* g;
+  void *m, *v;
+  float *m_scale, *v_scale, *master;
+  int64_t n;
+  int64_t vec;  // on 16-byte boundaries
+};
+// N tensors of a launch: a launch's arguments are copied on every call, so
+// few tensors take a smaller table.
+template <int N>
 struct Table {
-  void* p[kTable];
-  const void* g[kTable];
-  void* m[kTable];
-  void* v[kTable];
-  float* m_scale[kTable];
-  float* v_scale[kTable];
-  float* master[kTable];
-  int64_t n[kTable];
-  uint32_t first[kTable + 1];  // chunks before each tensor
-  uint8_t vec[kTable];         // on 16-byte boundaries
   int32_t count;
+  uint32_t first[N + 1];  // chunks before each tensor
+  Entry at[N];
 };
 
 struct Hyper {
@@ -175,8 +178,8 @@ __device__ __forceinline__ float encode(float (&x)[kVec], bool root) {
   return __fmul_rn(most, 1.0f / kTop);
 }
 
-template <class TP, class TG, bool MASTER, bool EIGHT>
-__global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ Table t, const Hyper h) {
+template <class TP, class TG, bool MASTER, bool EIGHT, int N>
+__global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ Table<N> t, const Hyper h) {
   const uint32_t chunk = blockIdx.x;
   int lo = 0, hi = t.count;  // the last tensor whose first chunk is at most `chunk`
   while (hi - lo > 1) {
@@ -186,26 +189,26 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
     else
       hi = mid;
   }
-  const int k = lo;
-  const bool vec = t.vec[k] != 0;
-  const int64_t i = int64_t(chunk - t.first[k]) * kChunk + threadIdx.x * kVec;
-  const int64_t rest = t.n[k] - i;
+  const Entry& x = t.at[lo];
+  const bool vec = x.vec != 0;
+  const int64_t i = int64_t(chunk - t.first[lo]) * kChunk + threadIdx.x * kVec;
+  const int64_t rest = x.n - i;
   const int left = rest > kVec ? kVec : rest < 0 ? 0 : static_cast<int>(rest);
   float g[kVec], p[kVec], m[kVec], v[kVec];
-  load8<TG>(t.g[k], i, left, vec, g);
+  load8<TG>(x.g, i, left, vec, g);
   if constexpr (MASTER)
-    load8<float>(t.master[k], i, left, vec, p);
+    load8<float>(x.master, i, left, vec, p);
   else
-    load8<TP>(t.p[k], i, left, vec, p);
+    load8<TP>(x.p, i, left, vec, p);
   if constexpr (EIGHT) {
     const int64_t block = i / ADAMW_BLOCK;
-    load_codes(t.m[k], i, left, vec, left > 0 ? t.m_scale[k][block] : 0.0f, m);
-    load_codes(t.v[k], i, left, vec, left > 0 ? t.v_scale[k][block] : 0.0f, v);
+    load_codes(x.m, i, left, vec, left > 0 ? x.m_scale[block] : 0.0f, m);
+    load_codes(x.v, i, left, vec, left > 0 ? x.v_scale[block] : 0.0f, v);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) v[j] = __fmul_rn(v[j], v[j]);
   } else {
-    load8<float>(t.m[k], i, left, vec, m);
-    load8<float>(t.v[k], i, left, vec, v);
+    load8<float>(x.m, i, left, vec, m);
+    load8<float>(x.v, i, left, vec, v);
   }
   if (h.grad_scale) {
     const float s = *h.grad_scale;
@@ -215,19 +218,19 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
   float r[kVec];
 #pragma unroll
   for (int j = 0; j < kVec; ++j) update(h, g[j], p[j], m[j], v[j], r[j]);
-  if constexpr (MASTER) store8<float>(t.master[k], i, left, vec, p);
-  store8<TP>(t.p[k], i, left, vec, p);
+  if constexpr (MASTER) store8<float>(x.master, i, left, vec, p);
+  store8<TP>(x.p, i, left, vec, p);
   if constexpr (EIGHT) {
     const float ms = encode(m, false), vs = encode(r, true);
-    store_codes(t.m[k], i, left, vec, m);
-    store_codes(t.v[k], i, left, vec, r);
+    store_codes(x.m, i, left, vec, m);
+    store_codes(x.v, i, left, vec, r);
     if (left > 0 && threadIdx.x % (ADAMW_BLOCK / kVec) == 0) {
-      t.m_scale[k][i / ADAMW_BLOCK] = ms;
-      t.v_scale[k][i / ADAMW_BLOCK] = vs;
+      x.m_scale[i / ADAMW_BLOCK] = ms;
+      x.v_scale[i / ADAMW_BLOCK] = vs;
     }
   } else {
-    store8<float>(t.m[k], i, left, vec, m);
-    store8<float>(t.v[k], i, left, vec, v);
+    store8<float>(x.m, i, left, vec, m);
+    store8<float>(x.v, i, left, vec, v);
   }
 }
 
@@ -235,17 +238,28 @@ namespace {
 
 bool placed(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
-template <class TP, class TG, bool MASTER>
-cudaError_t launch(const Table& t, const Hyper& h, bool eight, cudaStream_t s) {
+constexpr int kSmallTable = 48;
+
+template <class TP, class TG, bool MASTER, bool EIGHT>
+cudaError_t launch(const Table<kTable>& t, const Hyper& h, cudaStream_t s) {
   const uint32_t grid = t.first[t.count];
-  if (eight)
-    step_kernel<TP, TG, MASTER, true><<<grid, kThreads, 0, s>>>(t, h);
-  else
-    step_kernel<TP, TG, MASTER, false><<<grid, kThreads, 0, s>>>(t, h);
+  if (t.count <= kSmallTable) {
+    Table<kSmallTable> u;
+    u.count = t.count;
+    memcpy(u.first, t.first, sizeof(uint32_t) * (t.count + 1));
+    memcpy(u.at, t.at, sizeof(Entry) * t.count);
+    step_kernel<TP, TG, MASTER, EIGHT, kSmallTable><<<grid, kThreads, 0, s>>>(u, h);
+  } else {
+    step_kernel<TP, TG, MASTER, EIGHT, kTable><<<grid, kThreads, 0, s>>>(t, h);
+  }
   return cudaGetLastError();
 }
+template <class TP, class TG, bool MASTER>
+cudaError_t launch(const Table<kTable>& t, const Hyper& h, bool eight, cudaStream_t s) {
+  return eight ? launch<TP, TG, MASTER, true>(t, h, s) : launch<TP, TG, MASTER, false>(t, h, s);
+}
 
-cudaError_t launch_any(const Table& t, const Hyper& h, const adamw_opts* o, bool master, cudaStream_t s) {
+cudaError_t launch_any(const Table<kTable>& t, const Hyper& h, const adamw_opts* o, bool master, cudaStream_t s) {
   const bool eight = o->state_bits == 8, gb = o->g_dtype == B4_BF16;
   if (o->p_dtype == B4_F32)
     return gb ? launch<float, bf16_t, false>(t, h, eight, s) : launch<float, float, false>(t, h, eight, s);
@@ -300,8 +314,8 @@ extern "C" int adamw_step(const adamw_tensor* x, int32_t count, const adamw_opts
   h.grad_scale = o->grad_scale;
 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  Table tab;
-  memset(&tab, 0, sizeof(tab));
+  Table<kTable> tab;
+  tab.count = 0;
   for (int32_t k = 0; k < count; ++k) {
     if (x[k].n == 0) continue;
     // a tensor of more chunks than a grid holds is taken in pieces
@@ -315,16 +329,17 @@ extern "C" int adamw_step(const adamw_tensor* x, int32_t count, const adamw_opts
         tab.count = 0;
       }
       const int c = tab.count++;
-      tab.p[c] = static_cast<char*>(x[k].p) + at * pb;
-      tab.g[c] = static_cast<const char*>(x[k].g) + at * gb;
-      tab.m[c] = static_cast<char*>(x[k].m) + at * (eight ? 1 : 4);
-      tab.v[c] = static_cast<char*>(x[k].v) + at * (eight ? 1 : 4);
-      tab.m_scale[c] = eight ? x[k].m_scale + at / ADAMW_BLOCK : nullptr;
-      tab.v_scale[c] = eight ? x[k].v_scale + at / ADAMW_BLOCK : nullptr;
-      tab.master[c] = master ? x[k].master + at : nullptr;
-      tab.n[c] = n;
-      tab.vec[c] = placed(tab.p[c], 16) && placed(tab.g[c], 16) && placed(tab.m[c], eight ? 8 : 16) &&
-                   placed(tab.v[c], eight ? 8 : 16) && placed(tab.master[c], 16);
+      Entry& q = tab.at[c];
+      q.p = static_cast<char*>(x[k].p) + at * pb;
+      q.g = static_cast<const char*>(x[k].g) + at * gb;
+      q.m = static_cast<char*>(x[k].m) + at * (eight ? 1 : 4);
+      q.v = static_cast<char*>(x[k].v) + at * (eight ? 1 : 4);
+      q.m_scale = eight ? x[k].m_scale + at / ADAMW_BLOCK : nullptr;
+      q.v_scale = eight ? x[k].v_scale + at / ADAMW_BLOCK : nullptr;
+      q.master = master ? x[k].master + at : nullptr;
+      q.n = n;
+      q.vec = placed(q.p, 16) && placed(q.g, 16) && placed(q.m, eight ? 8 : 16) && placed(q.v, eight ? 8 : 16) &&
+              placed(q.master, 16);
       if (c == 0) tab.first[0] = 0;
       tab.first[c + 1] = tab.first[c] + chunks;
     }

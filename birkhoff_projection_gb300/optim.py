@@ -12,14 +12,20 @@ with one fp32 scale to 128 elements; the second moment is held as its root.
 """
 from __future__ import annotations
 
-import ctypes
+import struct
+from array import array
 
 import torch
 
-from . import _DT, _on_device
-from ._lib import ADAMW_BLOCK, AdamwOpts, AdamwTensor, check, lib
+from . import _DT
+from ._lib import ADAMW_BLOCK, check, lib
 
 __all__ = ["AdamW"]
+
+# adamw_tensor is eight 8-byte fields: p g m v m_scale v_scale master n
+_FIELDS = 8
+# adamw_opts: p_dtype g_dtype state_bits; lr beta1 beta2 eps weight_decay; step, grad_scale
+_OPTS = struct.Struct("<3i4x5dqQ")
 
 
 class AdamW(torch.optim.Optimizer):
@@ -58,6 +64,8 @@ class AdamW(torch.optim.Optimizer):
         """Allocate the packed state and each parameter's views of it."""
         every = [p for g in self.param_groups for p in g["params"]]
         device = every[0].device
+        if device.type != "cuda":
+            raise ValueError("parameters must be on one CUDA device")
         for p in every:
             if p.dtype not in _DT:
                 raise TypeError("parameters must be float32 or bfloat16, got %s" % p.dtype)
@@ -106,15 +114,14 @@ class AdamW(torch.optim.Optimizer):
                 params = [p for p in group["params"] if p.dtype == dtype and p.numel() > 0]
                 if not params:
                     continue
-                rows = (AdamwTensor * len(params))()
-                for r, p in zip(rows, params):
+                rows = array("Q")
+                for p in params:
                     s = self.state[p]
-                    r.m, r.v, r.n = s["exp_avg"].data_ptr(), s[self._second].data_ptr(), p.numel()
-                    if self.state_bits == 8:
-                        r.m_scale = s["exp_avg_scale"].data_ptr()
-                        r.v_scale = s["exp_avg_sq_root_scale"].data_ptr()
-                    if self.master_weights:
-                        r.master = s["master"].data_ptr()
+                    eight, master = self.state_bits == 8, self.master_weights
+                    rows.extend((0, 0, s["exp_avg"].data_ptr(), s[self._second].data_ptr(),
+                                 s["exp_avg_scale"].data_ptr() if eight else 0,
+                                 s["exp_avg_sq_root_scale"].data_ptr() if eight else 0,
+                                 s["master"].data_ptr() if master else 0, p.numel()))
                 self._plans.append((group, dtype, params, rows))
 
     def packed(self) -> dict:
@@ -135,34 +142,43 @@ class AdamW(torch.optim.Optimizer):
         if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1
                                        or grad_scale.device != self._device):
             raise ValueError("grad_scale must be one float32 on %s" % self._device)
-        calls = []
+        dev = self._device.index
+        calls = []  # the tables, and whatever they point to that is not kept elsewhere
         for group, dtype, params, rows in self._plans:
-            by_type = {}
-            for p, r in zip(params, rows):
-                g = p.grad
-                if g is None:
+            grads = [p.grad for p in params]
+            if any([g is None for g in grads]):  # (`in` would compare tensors)
+                some = [k for k, g in enumerate(grads) if g is not None]
+                params, grads = [params[k] for k in some], [grads[k] for k in some]
+                rows = array("Q", [v for k in some for v in rows[k * _FIELDS:(k + 1) * _FIELDS]])
+                if not some:
                     continue
-                if g.layout is not torch.strided or g.dtype not in _DT or g.device != self._device:
-                    raise ValueError("gradients must be dense float32 or bfloat16 tensors on %s" % self._device)
-                if not g.is_contiguous():
-                    g = g.contiguous()
-                r.p, r.g = p.data_ptr(), g.data_ptr()
-                by_type.setdefault(g.dtype, []).append((r, g))
-            for kind, some in by_type.items():
-                if len(some) == len(rows):
-                    table = rows
+            kinds = {g.dtype for g in grads}
+            if not kinds <= _DT.keys() or {g.get_device() for g in grads} != {dev} \
+                    or {g.layout for g in grads} != {torch.strided}:
+                raise ValueError("gradients must be dense float32 or bfloat16 tensors on %s" % self._device)
+            if not all([g.is_contiguous() for g in grads]):
+                grads = [g.contiguous() for g in grads]
+            table = rows[:]
+            view = memoryview(table)
+            view[0::_FIELDS] = memoryview(array("Q", [p.data_ptr() for p in params]))
+            view[1::_FIELDS] = memoryview(array("Q", [g.data_ptr() for g in grads]))
+            for kind in kinds:
+                if len(kinds) > 1:
+                    mine = array("Q", [v for k, g in enumerate(grads) if g.dtype == kind
+                                       for v in table[k * _FIELDS:(k + 1) * _FIELDS]])
                 else:
-                    table = (AdamwTensor * len(some))(*[r for r, _ in some])
-                calls.append((group, dtype, kind, table, [g for _, g in some]))
+                    mine = table
+                calls.append((group, dtype, kind, mine, grads))
         self.steps += 1
+        scale = 0 if grad_scale is None else grad_scale.data_ptr()
+        f = lib().adamw_step
         with torch.cuda.device(self._device):
-            stream = ctypes.c_void_p(torch.cuda.current_stream(self._device).cuda_stream)
+            stream = torch._C._cuda_getCurrentRawStream(dev)
             for group, dtype, kind, table, _ in calls:
                 beta1, beta2 = group["betas"]
-                opts = AdamwOpts(_DT[dtype], _DT[kind], self.state_bits, group["lr"], beta1, beta2, group["eps"],
-                                 group["weight_decay"], self.steps,
-                                 None if grad_scale is None else grad_scale.data_ptr())
-                check(lib().adamw_step(table, len(table), ctypes.byref(opts), stream), "adamw_step")
+                opts = _OPTS.pack(_DT[dtype], _DT[kind], self.state_bits, group["lr"], beta1, beta2, group["eps"],
+                                  group["weight_decay"], self.steps, scale)
+                check(f(table.buffer_info()[0], len(table) // _FIELDS, opts, stream), "adamw_step")
         return loss
 
     def state_dict(self):

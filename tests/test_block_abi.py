@@ -51,6 +51,22 @@ def test_structures_have_the_headers_fields_in_order(struct, name, cls):
     assert fields == list(cls._fields_)
 
 
+def test_packed_arguments_have_the_structures_layout():
+    kinds = {ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f", ctypes.c_void_p: "Q", ctypes.c_size_t: "Q"}
+    flat = re.sub(r"(\d+)(\w)", lambda m: m.group(2) * int(m.group(1)), block._ARGS.format[1:])
+    assert flat == "".join("Q" if k is ctypes.c_size_t or k is ctypes.c_void_p else kinds[k] for _, k in _lib.HcbArgs._fields_)
+    assert block._ARGS.size == ctypes.sizeof(_lib.HcbArgs)
+    numbers = list(range(1, len(flat) + 1))
+    args = _lib.HcbArgs.from_buffer_copy(block._ARGS.pack(*numbers))
+    assert [getattr(args, n) for n, _ in _lib.HcbArgs._fields_] == numbers
+
+
+def test_packed_optimizer_arguments_have_the_structures_layout():
+    assert ctypes.sizeof(_lib.AdamwTensor) == 8 * optim._FIELDS
+    o = _lib.AdamwOpts.from_buffer_copy(optim._OPTS.pack(*range(1, 11)))
+    assert [getattr(o, n) for n, _ in _lib.AdamwOpts._fields_] == list(range(1, 11))
+
+
 def test_constants_match():
     text = open(os.path.join(ROOT, "include", "hc_block.h")).read() + open(os.path.join(ROOT, "include", "adamw.h")).read()
     for name in ("HCB_MAX_STREAMS", "HCB_MAX_CHANNELS", "HCB_ACT_NONE", "HCB_ACT_SIGMOID", "HCB_ACT_SILU",

@@ -95,11 +95,12 @@ def test_steps(dtype, gtype, master, bits):
         else:  # a parameter's .grad has its type: the C entry takes any pair
             (_, _, some, rows), = opt._plans
             some_grads = [g for g in grads if g.numel()]
-            for r, p, g in zip(rows, some, some_grads):
-                r.p, r.g = p.data_ptr(), g.data_ptr()
+            table = (_lib.AdamwTensor * len(some))(*[
+                _lib.AdamwTensor(p.data_ptr(), g.data_ptr(), *rows[8 * k + 2:8 * k + 8])
+                for k, (p, g) in enumerate(zip(some, some_grads))])
             o = _lib.AdamwOpts(_DT[dtype], _DT[gtype], bits, HYPER["lr"], *HYPER["betas"], HYPER["eps"],
                                HYPER["weight_decay"], t + 1, None)
-            _lib.check(_lib.lib().adamw_step(rows, len(rows), ctypes.byref(o), None), "adamw_step")
+            _lib.check(_lib.lib().adamw_step(table, len(table), ctypes.byref(o), None), "adamw_step")
             torch.cuda.synchronize()
         twin.step(params, opt, grads, **HYPER)
 

@@ -9,12 +9,14 @@ gradient at most 40 + 16 more over CTAs, and a result multiplies up to three
 such sums and a handful of rounded factors.  The 2-norm of the error is held
 to 16 2^-24 of the magnitudes' (roundings of either sign: the root of N).
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import birkhoff_projection_gb300 as b4
-from birkhoff_projection_gb300 import block
+from birkhoff_projection_gb300 import _lib, block
 from oracle import block as ob
 
 pytestmark = pytest.mark.gpu
@@ -61,6 +63,23 @@ def inputs(T, S, C, tx, ty, act="sigmoid", mix=True, coef=F, weight=F, seed=0):
     k["w2"] = rnd(seed + 7, C, dtype=weight, std=0.2, mean=1.0)
     k["D"], k["dh"] = rnd(seed + 8, T, S, C, dtype=tx), rnd(seed + 9, T, C, dtype=ty)
     return k
+
+
+def direct(entry, tensors, T, S, C, dtype, act=0):
+    """A call of the C entry with contiguous tensors of one type, fp32 coefficients and weights."""
+    kind = 1 if dtype == H else 0
+    args = _lib.HcbArgs(T=T, S=S, C=C, x_dtype=kind, y_dtype=kind, act=act, norm=1, eps=1e-6, scale=1.0)
+    for name, t in tensors.items():
+        if t is not None:
+            setattr(args, name, t.data_ptr())
+    for name in ("x", "dout", "dres"):
+        setattr(args, name + "_ts", S * C)
+        setattr(args, name + "_ss", C)
+    for name, n in (("y", C), ("gate", C), ("dh", C), ("P", S * S), ("a", S), ("b", S)):
+        setattr(args, name + "_ts", n)
+    if tensors.get("workspace") is not None:
+        args.workspace_bytes = tensors["workspace"].numel()
+    _lib.check(getattr(_lib.lib(), entry)(ctypes.byref(args), torch.cuda.current_stream().cuda_stream), entry)
 
 
 def everything(k, act="sigmoid", norm=True, scale=0.5, eps=1e-6, eps2=1e-5):
@@ -247,17 +266,8 @@ def test_gradients_may_replace_their_inputs():
     T, S, C = 21, 4, 320
     k = inputs(T, S, C, H, H)
     want = block.enter_backward(k["dh"], k["x"], k["a"], k["w"], dres=k["D"])
-    c = block._Call(k["x"])
-    c.y_type(H, "dh")
-    c.args.eps = 1e-6
     res = k["D"].clone()
-    c.streams(k["x"], "x", "x", "x_ts", "x_ss")
-    c.row(k["dh"], "dh", "dh", "dh_ts")
-    c.coefficients(k["a"], "a", "a", "a_dtype", "a_ts", (S,))
-    c.weight(k["w"], "weight", "w", "w_dtype")
-    c.streams(res, "dres", "dres", "dres_ts", "dres_ss")
-    c.args.dx = res.data_ptr()
-    c.run("hcb_enter_backward")
+    direct("hcb_enter_backward", dict(x=k["x"], dh=k["dh"], a=k["a"], w=k["w"], dres=res, dx=res), T, S, C, H)
     assert torch.equal(res, want.dx)
 
 
@@ -267,15 +277,10 @@ def test_every_gradient_alone():
     k = inputs(T, S, C, F, F)
     want = block.leave_backward(k["D"], k["x"], k["y"], k["P"], k["b"], gate=k["gate"], weight=k["w"])
     for field, name in (("dx", "dx"), ("dy", "dy"), ("dP", "dP"), ("db", "db"), ("dgate", "dgate"), ("dw", "dweight")):
-        c = block._Call(k["x"])
-        block._leave_inputs(c, k["x"], k["y"], k["P"], k["b"], k["gate"], "sigmoid", k["w"], True, 1.0, 1e-6)
-        c.streams(k["D"], "dout", "dout", "dout_ts", "dout_ss")
-        c.streams(k["x"], "x", "x", "x_ts", "x_ss")
         t = torch.full_like(getattr(want, name), 7.0)
-        setattr(c.args, field, t.data_ptr())
-        if field == "dw":
-            c.scratch(None, 1)
-        c.run("hcb_leave_backward")
+        ws = torch.empty(block.workspace_bytes(T, C), dtype=torch.uint8, device=DEV) if field == "dw" else None
+        direct("hcb_leave_backward", dict(dout=k["D"], x=k["x"], y=k["y"], P=k["P"], b=k["b"], gate=k["gate"], w=k["w"],
+                                          workspace=ws, **{field: t}), T, S, C, F, act=1)
         assert torch.equal(t, getattr(want, name)), name
 
 
