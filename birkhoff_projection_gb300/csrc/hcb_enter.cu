@@ -8,6 +8,12 @@
 #ifndef HCB_ENTER_BWD_DEPTH
 #define HCB_ENTER_BWD_DEPTH 2
 #endif
+#ifndef HCB_ENTER_PER
+#define HCB_ENTER_PER 2
+#endif
+#ifndef HCB_ENTER_BWD_PER
+#define HCB_ENTER_BWD_PER 2
+#endif
 
 namespace hcb {
 
@@ -20,13 +26,14 @@ struct Enter {
   using Co = Coefficients<SP, false, false, true>;
   using Sum = GroupSum<1>;
   static constexpr int DEPTH = HCB_ENTER_DEPTH;
-  static size_t bytes(int S, int C, int G) {
-    return size_t(G) * (DEPTH * S * RX::SLOT + items(C, V, G) * V * 4) +
-           4 * (G / 32 * Co::FLOATS + (Sum::floats(G) + 3) / 4 * 4);
+  static constexpr int SLOT = SP * RX::SLOT;    // the streams
+  static constexpr int ITEM = kFloats<V>;       // u
+  static Need need(int G, int) {
+    return {DEPTH * SLOT, ITEM, 4 * (G / 32 * Co::FLOATS + Sum::floats(G))};
   }
 };
 
-template <int SP, class TX, class TY, int V, bool ODD>
+template <int SP, bool EXACT, class TX, class TY, int V, bool ODD>
 __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
   using E = Enter<SP, TX, TY, V, ODD>;
   using RX = typename E::RX;
@@ -35,38 +42,40 @@ __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
   constexpr int DEPTH = E::DEPTH;
   extern __shared__ __align__(16) char smem[];
   const int G = p.G, NG = blockDim.x / G, group = threadIdx.x / G, l = threadIdx.x % G;
-  const int lane = threadIdx.x & 31, warp = l / 32, C = p.C, S = p.S;
-  const int K = (C + V * G - 1) / (V * G);
-  char* ring = smem + size_t(group) * p.group_bytes;
-  float* u_s = reinterpret_cast<float*>(ring + DEPTH * G * S * RX::SLOT);
-  float* co_s = u_s + K * V * G + warp * Co::FLOATS;
-  float* red = u_s + K * V * G + G / 32 * Co::FLOATS;
+  const int lane = threadIdx.x & 31, warp = l / 32, C = p.C, S = EXACT ? SP : p.S, GV = G * V;
+  const int K = (C + GV - 1) / GV;
+  char* of_group = smem + group * p.group_bytes;
+  char* ring = of_group + warp * p.warp_bytes;
+  char* item0 = ring + DEPTH * E::SLOT;
+  float* co_all = reinterpret_cast<float*>(of_group + G / 32 * p.warp_bytes);
+  float* co_s = co_all + warp * Co::FLOATS;
+  float* red = co_all + G / 32 * Co::FLOATS;
   int turn = 0;
   const float inv_c = 1.0f / static_cast<float>(C);
   const int64_t step = int64_t(gridDim.x) * NG;
   int64_t t = int64_t(blockIdx.x) * NG + group;
 
   int64_t ta = t;  // the next item to copy
-  int ka = 0, slot_a = 0;
+  int ca = l * V, ka = 0;
+  char* slot_a = ring;
+  const TX* xa = static_cast<const TX*>(p.x) + ta * p.x_ts;
   auto copy_next = [&] {
-    const int c = (ka * G + l) * V;
-    if (ta < p.T && c < C) {
-      const TX* x = static_cast<const TX*>(p.x) + ta * p.x_ts + c;
-      char* s = ring + slot_a * G * S * RX::SLOT;
+    if (ta < p.T && ca < C) {
 #pragma unroll
       for (int i = 0; i < SP; ++i)
-        if (i < S) RX::copy(s + i * G * RX::SLOT, G, l, x + i * p.x_ss, C - c);
+        if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, xa + i * p.x_ss + ca, C - ca);
     }
     copy_commit();
-    if (++ka == K) ka = 0, ta += step;
-    if (++slot_a == DEPTH) slot_a = 0;
+    ca += GV;
+    if (++ka == K) ka = 0, ca = l * V, ta += step, xa = static_cast<const TX*>(p.x) + ta * p.x_ts;
+    slot_a = slot_a == ring + (DEPTH - 1) * E::SLOT ? ring : slot_a + E::SLOT;
   };
   Co co;
   if (t < p.T) co.fetch(p, t, lane);
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) copy_next();
 
-  int slot = 0;
+  const char* slot = ring;
   for (; t < p.T; t += step) {
     co.spread(co_s, lane);
     if (t + step < p.T) co.fetch(p, t + step, lane);
@@ -74,45 +83,44 @@ __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
     Co::read(co_s, Co::NB, a);
     const TX* x = static_cast<const TX*>(p.x) + t * p.x_ts;
     float ss[1] = {0.0f};
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * G + l) * V;
+    char* item = item0;
+    for (int c = l * V, k = 0; k < K; ++k, c += GV, item += E::ITEM) {
       copy_wait<DEPTH - 1>();
       float u[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) u[j] = 0.0f;
       if (c < C) {
-        const char* s = ring + slot * G * S * RX::SLOT;
 #pragma unroll
         for (int i = 0; i < SP; ++i) {
-          if (i < S) {
+          if (EXACT || i < S) {
             float xv[V];
-            RX::arrived(s + i * G * RX::SLOT, G, l, x + i * p.x_ss + c, xv);
+            RX::arrived(slot + i * RX::SLOT, lane, x + i * p.x_ss + c, xv);
 #pragma unroll
             for (int j = 0; j < V; ++j) u[j] += a[i] * xv[j];
           }
         }
       }
       copy_next();
-      if (++slot == DEPTH) slot = 0;
+      slot = slot == ring + (DEPTH - 1) * E::SLOT ? ring : slot + E::SLOT;
 #pragma unroll
       for (int j = 0; j < V; ++j) ss[0] += u[j] * u[j];
-      keep<V>(u_s, G, l, k, u);
+      keep<V>(item, lane, u);
     }
     float total[1];
     GroupSum<1>::run(ss, total, red, turn, G, group, lane, warp);
     const float r = rsqrtf(of_total(total, 0) * inv_c + p.eps);
     TY* h = static_cast<TY*>(p.h) + t * C;
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * G + l) * V;
-      if (c >= C) break;
+    item = item0;
+    for (int c = l * V; c < C; c += GV, item += E::ITEM) {
       float u[V], w[V];
-      kept<V>(u_s, G, l, k, u);
+      kept<V>(item, lane, u);
       p.w.load<V, ODD>(c, C - c, w);
 #pragma unroll
       for (int j = 0; j < V; ++j) u[j] *= r * w[j];
       RY::store(h + c, u, C - c);
     }
   }
+  copy_wait_all();
 }
 
 // With G = w dh all sums of the gradient are linear in <G, x_s> and <u, x_s>:
@@ -126,14 +134,16 @@ struct EnterBackward {
   using Co = Coefficients<SP, false, false, true>;
   using Sum = GroupSum<2 * SP>;
   static constexpr int DEPTH = HCB_ENTER_BWD_DEPTH;
-  static __host__ __device__ constexpr int slot(int S) { return S * RX::SLOT + RY::SLOT; }
-  static size_t bytes(int S, int C, int G, bool dw) {
-    return size_t(G) * (DEPTH * slot(S) + items(C, V, G) * V * (4 + sizeof(TY) + (dw ? 4 : 0))) +
-           4 * (G / 32 * Co::FLOATS + (Sum::floats(G) + 3) / 4 * 4);
+  // a slot: the streams (or dres), then dh
+  static constexpr int DH = SP * RX::SLOT, SLOT = DH + RY::SLOT;
+  // kept: u, dh, and the weight's share
+  static constexpr int KH = kFloats<V>, KW = KH + RY::KEPT, ITEM = KW + kFloats<V>;
+  static Need need(int G, int direct) {
+    return {DEPTH * SLOT, direct ? KW : ITEM, 4 * (G / 32 * Co::FLOATS + Sum::floats(G))};
   }
 };
 
-template <int SP, class TX, class TY, int V, bool ODD>
+template <int SP, bool EXACT, class TX, class TY, int V, bool ODD>
 __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Params p) {
   using E = EnterBackward<SP, TX, TY, V, ODD>;
   using RX = typename E::RX;
@@ -143,17 +153,16 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
   constexpr int DEPTH = E::DEPTH;
   extern __shared__ __align__(16) char smem[];
   const int G = p.G, NG = blockDim.x / G, group = threadIdx.x / G, l = threadIdx.x % G;
-  const int lane = threadIdx.x & 31, warp = l / 32, C = p.C, S = p.S;
-  const int K = (C + V * G - 1) / (V * G);
-  const int slot_bytes = G * E::slot(S);
-  char* ring = smem + size_t(group) * p.group_bytes;
-  float* u_s = reinterpret_cast<float*>(ring + DEPTH * slot_bytes);
-  char* dh_s = reinterpret_cast<char*>(u_s + K * V * G);
-  float* co_all = reinterpret_cast<float*>(dh_s + K * V * G * sizeof(TY));
+  const int lane = threadIdx.x & 31, warp = l / 32, C = p.C, S = EXACT ? SP : p.S, GV = G * V;
+  const int K = (C + GV - 1) / GV;
+  const int ITEM = p.direct ? E::KW : E::ITEM;
+  char* of_group = smem + group * p.group_bytes;
+  char* ring = of_group + warp * p.warp_bytes;
+  char* item0 = ring + DEPTH * E::SLOT;
+  float* co_all = reinterpret_cast<float*>(of_group + G / 32 * p.warp_bytes);
   float* co_s = co_all + warp * Co::FLOATS;
   float* red = co_all + G / 32 * Co::FLOATS;
-  WeightShare<V> dw = {red + (Sum::floats(G) + 3) / 4 * 4,
-                       p.direct ? p.dw + int64_t(blockIdx.x) * pitch(C) : nullptr};
+  float* row_dw = p.direct && p.dw ? p.dw + int64_t(blockIdx.x) * pitch(C) : nullptr;
   int turn = 0;
   const float inv_c = 1.0f / static_cast<float>(C);
   const int64_t step = int64_t(gridDim.x) * NG;
@@ -162,32 +171,43 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
   // items of a token: x and dh for every k, then, if there is one, dres
   const int NI = p.dres ? 2 * K : K;
   int64_t ta = t;
-  int ia = 0, slot_a = 0;
+  int ca = l * V, ia = 0;
+  char* slot_a = ring;
   auto copy_next = [&] {
     const bool second = ia >= K;
-    const int c = ((second ? ia - K : ia) * G + l) * V;
-    if (ta < p.T && c < C) {
-      char* s = ring + slot_a * slot_bytes;
-      const TX* x = second ? static_cast<const TX*>(p.dres) + ta * p.dres_ts + c
-                           : static_cast<const TX*>(p.x) + ta * p.x_ts + c;
+    if (ta < p.T && ca < C) {
+      const TX* x = second ? static_cast<const TX*>(p.dres) + ta * p.dres_ts
+                           : static_cast<const TX*>(p.x) + ta * p.x_ts;
       const int64_t ss = second ? p.dres_ss : p.x_ss;
 #pragma unroll
       for (int i = 0; i < SP; ++i)
-        if (i < S) RX::copy(s + i * G * RX::SLOT, G, l, x + i * ss, C - c);
+        if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, x + i * ss + ca, C - ca);
       if (!second)
-        RY::copy(s + S * G * RX::SLOT, G, l, static_cast<const TY*>(p.dh) + ta * p.dh_ts + c, C - c);
+        RY::copy(slot_a + E::DH, lane, static_cast<const TY*>(p.dh) + ta * p.dh_ts + ca, C - ca);
     }
     copy_commit();
-    if (++ia == NI) ia = 0, ta += step;
-    if (++slot_a == DEPTH) slot_a = 0;
+    ca += GV;
+    ++ia;
+    if (ia == K) ca = l * V;
+    if (ia == NI) ia = 0, ca = l * V, ta += step;
+    slot_a = slot_a == ring + (DEPTH - 1) * E::SLOT ? ring : slot_a + E::SLOT;
   };
   Co co;
   if (t < p.T) co.fetch(p, t, lane);
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) copy_next();
-  if (p.dw) dw.zero(G, l, K, C);
+  if (p.dw) {
+    const float z[V] = {};
+    char* item = item0;
+    for (int c = l * V; c < C; c += GV, item += ITEM) {
+      if (row_dw)
+        keep<V, 16>(reinterpret_cast<char*>(row_dw + c), 0, z);
+      else
+        keep<V>(item + E::KW, lane, z);
+    }
+  }
 
-  int slot = 0;
+  const char* slot = ring;
   for (; t < p.T; t += step) {
     co.spread(co_s, lane);
     if (t + step < p.T) co.fetch(p, t + step, lane);
@@ -198,28 +218,24 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
     float sum[2 * SP];
 #pragma unroll
     for (int s = 0; s < 2 * SP; ++s) sum[s] = 0.0f;
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * G + l) * V;
-      float xv[SP][V], g[V], w[V], u[V];
+    char* item = item0;
+    for (int c = l * V, k = 0; k < K; ++k, c += GV, item += ITEM) {
+      float w[V];
       if (c < C) p.w.load<V, ODD>(c, C - c, w);
       copy_wait<DEPTH - 1>();
       if (c < C) {
-        const char* s = ring + slot * slot_bytes;
+        float xv[SP][V], g[V], u[V];
 #pragma unroll
         for (int i = 0; i < SP; ++i) {
-          if (i < S) {
-            RX::arrived(s + i * G * RX::SLOT, G, l, x + i * p.x_ss + c, xv[i]);
+          if (EXACT || i < S) {
+            RX::arrived(slot + i * RX::SLOT, lane, x + i * p.x_ss + c, xv[i]);
           } else {
 #pragma unroll
             for (int j = 0; j < V; ++j) xv[i][j] = 0.0f;
           }
         }
-        RY::arrived(s + S * G * RX::SLOT, G, l, dh + c, g);
-      }
-      copy_next();
-      if (++slot == DEPTH) slot = 0;
-      if (c < C) {
-        keep_row<TY, V>(dh_s, G, l, k, g);
+        RY::arrived(slot + E::DH, lane, dh + c, g);
+        RY::keep(item + E::KH, lane, g);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           g[j] *= w[j];
@@ -232,8 +248,10 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
             sum[SP + s] += u[j] * xv[s][j];
           }
         }
-        keep<V>(u_s, G, l, k, u);
+        keep<V>(item, lane, u);
       }
+      copy_next();
+      slot = slot == ring + (DEPTH - 1) * E::SLOT ? ring : slot + E::SLOT;
     }
     float total[1];
     Sum::run(sum, total, red, turn, G, group, lane, warp);
@@ -250,62 +268,51 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
       if (warp == 0 && lane < S) put_any(p.da, p.a.bf16, t * S + lane, r * (total[0] - k_u * u_x));
     }
     const TX* dres = p.dres ? static_cast<const TX*>(p.dres) + t * p.dres_ts : nullptr;
-    TX* dx = static_cast<TX*>(p.dx) + t * S * C;
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * G + l) * V;
-      float u[V], g[V], w[V];
+    TX* dx = p.dx ? static_cast<TX*>(p.dx) + t * S * C : nullptr;
+    item = item0;
+    for (int c = l * V, k = 0; k < K; ++k, c += GV, item += ITEM) {
+      if (dres) copy_wait<DEPTH - 1>();
       if (c < C) {
-        kept<V>(u_s, G, l, k, u);
-        kept_row<TY, V>(dh_s, G, l, k, g);
+        float u[V], g[V], w[V];
+        kept<V>(item, lane, u);
+        RY::kept(item + E::KH, lane, g);
         p.w.load<V, ODD>(c, C - c, w);
         if (p.dw) {
           float d[V];
 #pragma unroll
           for (int j = 0; j < V; ++j) d[j] = g[j] * (u[j] * r);
-          dw.add(G, l, k, d);
+          add_share<V>(item + E::KW, lane, row_dw ? row_dw + c : nullptr, d);
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) u[j] = r * (g[j] * w[j] - k_u * u[j]);
-      }
-      if (dres) {
-        copy_wait<DEPTH - 1>();
-        if (c < C) {
-          const char* s = ring + slot * slot_bytes;
-          float d[SP][V];
-#pragma unroll
-          for (int i = 0; i < SP; ++i)
-            if (i < S) RX::arrived(s + i * G * RX::SLOT, G, l, dres + i * p.dres_ss + c, d[i]);
-          copy_next();
+        if (dx) {
 #pragma unroll
           for (int i = 0; i < SP; ++i) {
-            if (i < S) {
+            if (EXACT || i < S) {
+              float d[V];
+              if (dres) {
+                RX::arrived(slot + i * RX::SLOT, lane, dres + i * p.dres_ss + c, d);
 #pragma unroll
-              for (int j = 0; j < V; ++j) d[i][j] += a[i] * u[j];
-              RX::store(dx + int64_t(i) * C + c, d[i], C - c);
+                for (int j = 0; j < V; ++j) d[j] += a[i] * u[j];
+              } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) d[j] = a[i] * u[j];
+              }
+              RX::store(dx + i * C + c, d, C - c);
             }
           }
-        } else {
-          copy_next();
         }
-        if (++slot == DEPTH) slot = 0;
-      } else if (c < C && p.dx) {
-#pragma unroll
-        for (int i = 0; i < SP; ++i) {
-          if (i < S) {
-            float d[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) d[j] = a[i] * u[j];
-            RX::store(dx + int64_t(i) * C + c, d, C - c);
-          }
-        }
+      }
+      if (dres) {
+        copy_next();
+        slot = slot == ring + (DEPTH - 1) * E::SLOT ? ring : slot + E::SLOT;
       }
     }
   }
   copy_wait_all();
   if (p.dw && !p.direct) {
     __syncthreads();
-    sum_shares<V>(reinterpret_cast<float*>(reinterpret_cast<char*>(dw.s) - size_t(group) * p.group_bytes),
-                  p.group_bytes / 4, G, NG, C, p.dw + int64_t(blockIdx.x) * pitch(C));
+    sum_shares<V>(smem + DEPTH * E::SLOT + E::KW, p, G, NG, ITEM, p.dw + int64_t(blockIdx.x) * pitch(C));
   }
 }
 
@@ -314,28 +321,22 @@ namespace {
 struct Forward {
   const Params& p;
   cudaStream_t s;
-  template <int SP, class TX, class TY, int V, bool ODD>
+  template <int SP, bool EXACT, class TX, class TY, int V, bool ODD>
   cudaError_t operator()() const {
-    using E = Enter<SP, TX, TY, V, ODD>;
-    int direct, grid;
-    const Shape sh = fitted(shape_of(p.T, p.C, V, kMaxGroup), false, &direct,
-                            [&](int G, bool) { return E::bytes(p.S, p.C, G); });
-    return launch<enter_kernel<SP, TX, TY, V, ODD>>(p, sh, E::bytes(p.S, p.C, sh.G), 1 << 30, &grid, s);
+    int grid;
+    return launch<enter_kernel<SP, EXACT, TX, TY, V, ODD>>(
+        p, shape_of(p.T, p.C, V, HCB_ENTER_PER, kMaxGroup), V, Enter<SP, TX, TY, V, ODD>::need, 1 << 30, &grid, s);
   }
 };
 struct Backward {
   const Params& p;
   int* rows;
   cudaStream_t s;
-  template <int SP, class TX, class TY, int V, bool ODD>
+  template <int SP, bool EXACT, class TX, class TY, int V, bool ODD>
   cudaError_t operator()() const {
-    using E = EnterBackward<SP, TX, TY, V, ODD>;
-    Params q = p;
-    const bool dw = p.dw != nullptr;
-    const Shape sh = fitted(shape_of(p.T, p.C, V, kMaxGroup), dw, &q.direct,
-                            [&](int G, bool direct) { return E::bytes(p.S, p.C, G, dw && !direct); });
-    return launch<enter_backward_kernel<SP, TX, TY, V, ODD>>(
-        q, sh, E::bytes(p.S, p.C, sh.G, dw && !q.direct), dw ? kMaxRows : 1 << 30, rows, s);
+    return launch<enter_backward_kernel<SP, EXACT, TX, TY, V, ODD>>(
+        p, shape_of(p.T, p.C, V, HCB_ENTER_BWD_PER, kMaxGroup), V, EnterBackward<SP, TX, TY, V, ODD>::need,
+        p.dw ? kMaxRows : 1 << 30, rows, s);
   }
 };
 

@@ -6,6 +6,9 @@
 #ifndef HCB_LEAVE_DEPTH
 #define HCB_LEAVE_DEPTH 2
 #endif
+#ifndef HCB_LEAVE_PER
+#define HCB_LEAVE_PER 2
+#endif
 
 namespace hcb {
 
@@ -19,21 +22,17 @@ struct Leave {
   using Co = Coefficients<SP, true, true, true>;
   using Sum = GroupSum<1>;
   static constexpr int DEPTH = HCB_LEAVE_DEPTH;
-  // y and the gate take the streams' place in a slot where both have vectors
-  // of one size; otherwise a thread's part of a slot would not be its own for
-  // both kinds of items, and they lie behind the streams
-  static constexpr bool SHARED = RX::SLOT == RY::SLOT;
-  static __host__ __device__ constexpr int y_at(int S) { return SHARED ? 0 : S * RX::SLOT; }
-  static __host__ __device__ constexpr int slot(int S) {
-    return SHARED && S >= 2 ? S * RX::SLOT : y_at(S) + 2 * RY::SLOT;
-  }
-  static size_t bytes(int S, int C, int G) {
-    return size_t(G) * (DEPTH * slot(S) + items(C, V, G) * V * 4) +
-           4 * (G / 32 * Co::FLOATS + 2 * ((Sum::floats(G) + 3) / 4 * 4));
+  // a slot: the streams, or y and the gate; in one place only where both have
+  // planes of one size, so that a lane's bytes are its own in both
+  static constexpr int Y = RX::SLOT == RY::SLOT ? 0 : SP * RX::SLOT;
+  static constexpr int SLOT = SP * RX::SLOT > Y + 2 * RY::SLOT ? SP * RX::SLOT : Y + 2 * RY::SLOT;
+  static constexpr int ITEM = kFloats<V>;  // kept: w act y, then u
+  static Need need(int G, int) {
+    return {DEPTH * SLOT, ITEM, 4 * (G / 32 * Co::FLOATS + 2 * Sum::floats(G))};
   }
 };
 
-template <int SP, class TX, class TY, int V, bool ODD>
+template <int SP, bool EXACT, class TX, class TY, int V, bool ODD>
 __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(const Params p) {
   using E = Leave<SP, TX, TY, V, ODD>;
   using RX = typename E::RX;
@@ -42,75 +41,72 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
   constexpr int DEPTH = E::DEPTH;
   extern __shared__ __align__(16) char smem[];
   const int G = p.G, NG = blockDim.x / G, group = threadIdx.x / G, l = threadIdx.x % G;
-  const int lane = threadIdx.x & 31, warp = l / 32, C = p.C, S = p.S;
-  const int K = (C + V * G - 1) / (V * G);
-  const int slot_bytes = G * E::slot(S);
-  char* ring = smem + size_t(group) * p.group_bytes;
-  float* u_s = reinterpret_cast<float*>(ring + DEPTH * slot_bytes);  // w act y, then u
-  float* co_s = u_s + K * V * G + warp * Co::FLOATS;
-  float* red = u_s + K * V * G + G / 32 * Co::FLOATS;
-  float* red_next = red + (GroupSum<1>::floats(G) + 3) / 4 * 4;
+  const int lane = threadIdx.x & 31, warp = l / 32, C = p.C, S = EXACT ? SP : p.S, GV = G * V;
+  const int K = (C + GV - 1) / GV;
+  char* of_group = smem + group * p.group_bytes;
+  char* ring = of_group + warp * p.warp_bytes;
+  char* item0 = ring + DEPTH * E::SLOT;
+  float* co_all = reinterpret_cast<float*>(of_group + G / 32 * p.warp_bytes);
+  float* co_s = co_all + warp * Co::FLOATS;
+  float* red = co_all + G / 32 * Co::FLOATS;
+  float* red_next = red + GroupSum<1>::floats(G);
   int turn = 0, turn_next = 0;
   const float inv_c = 1.0f / static_cast<float>(C);
-  const bool mix = p.P.p != nullptr;
+  const bool mix = p.P.p != nullptr, gated = p.gate != nullptr;
   const int64_t step = int64_t(gridDim.x) * NG;
   int64_t t = int64_t(blockIdx.x) * NG + group;
 
   int64_t ta = t;
-  int ia = 0, slot_a = 0;
+  int ca = l * V, ia = 0;
+  char* slot_a = ring;
   auto copy_next = [&] {
-    const bool second = ia >= K;
-    const int c = ((second ? ia - K : ia) * G + l) * V;
-    if (ta < p.T && c < C) {
-      char* s = ring + slot_a * slot_bytes;
-      if (second) {
-        const TX* x = static_cast<const TX*>(p.x) + ta * p.x_ts + c;
+    if (ta < p.T && ca < C) {
+      if (ia >= K) {
+        const TX* x = static_cast<const TX*>(p.x) + ta * p.x_ts + ca;
 #pragma unroll
         for (int i = 0; i < SP; ++i)
-          if (i < S) RX::copy(s + i * G * RX::SLOT, G, l, x + i * p.x_ss, C - c);
+          if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, x + i * p.x_ss, C - ca);
       } else {
-        s += G * E::y_at(S);
-        RY::copy(s, G, l, static_cast<const TY*>(p.y) + ta * p.y_ts + c, C - c);
-        if (p.gate)
-          RY::copy(s + G * RY::SLOT, G, l, static_cast<const TY*>(p.gate) + ta * p.gate_ts + c, C - c);
+        RY::copy(slot_a + E::Y, lane, static_cast<const TY*>(p.y) + ta * p.y_ts + ca, C - ca);
+        if (gated) RY::copy(slot_a + E::Y + RY::SLOT, lane, static_cast<const TY*>(p.gate) + ta * p.gate_ts + ca, C - ca);
       }
     }
     copy_commit();
-    if (++ia == 2 * K) ia = 0, ta += step;
-    if (++slot_a == DEPTH) slot_a = 0;
+    ca += GV;
+    ++ia;
+    if (ia == K) ca = l * V;
+    if (ia == 2 * K) ia = 0, ca = l * V, ta += step;
+    slot_a = slot_a == ring + (DEPTH - 1) * E::SLOT ? ring : slot_a + E::SLOT;
   };
   Co co;
   if (t < p.T) co.fetch(p, t, lane);
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) copy_next();
 
-  int slot = 0;
+  const char* slot = ring;
   for (; t < p.T; t += step) {
     co.spread(co_s, lane);
     if (t + step < p.T) co.fetch(p, t + step, lane);
     const TX* x = static_cast<const TX*>(p.x) + t * p.x_ts;
     const TY* y = static_cast<const TY*>(p.y) + t * p.y_ts;
-    const TY* gate = p.gate ? static_cast<const TY*>(p.gate) + t * p.gate_ts : nullptr;
+    const TY* gate = static_cast<const TY*>(p.gate) + t * p.gate_ts;
     float ss[1] = {0.0f};
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * G + l) * V;
-      float v[V], g[V], w[V];
+    char* item = item0;
+    for (int c = l * V, k = 0; k < K; ++k, c += GV, item += E::ITEM) {
+      float w[V];
       if (c < C) p.w.load<V, ODD>(c, C - c, w);
       copy_wait<DEPTH - 1>();
       if (c < C) {
-        const char* s = ring + slot * slot_bytes + G * E::y_at(S);
-        RY::arrived(s, G, l, y + c, v);
-        if (gate) RY::arrived(s + G * RY::SLOT, G, l, gate + c, g);
-      }
-      copy_next();
-      if (++slot == DEPTH) slot = 0;
-      if (c < C) {
+        float v[V];
+        RY::arrived(slot + E::Y, lane, y + c, v);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           ss[0] += v[j] * v[j];
           v[j] *= w[j];
         }
-        if (gate) {
+        if (gated) {
+          float g[V];
+          RY::arrived(slot + E::Y + RY::SLOT, lane, gate + c, g);
 #pragma unroll
           for (int j = 0; j < V; ++j) {
             float q, slope;
@@ -118,8 +114,10 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
             v[j] *= q;
           }
         }
-        keep<V>(u_s, G, l, k, v);
+        keep<V>(item, lane, v);
       }
+      copy_next();
+      slot = slot == ring + (DEPTH - 1) * E::SLOT ? ring : slot + E::SLOT;
     }
     float rho = p.scale;
     if (p.norm) {
@@ -137,32 +135,26 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
     }
     TX* out = static_cast<TX*>(p.out) + t * S * C;
     ss[0] = 0.0f;
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * G + l) * V;
-      float v[V], xv[SP][V];
-      if (c < C) kept<V>(u_s, G, l, k, v);
+    item = item0;
+    for (int c = l * V, k = 0; k < K; ++k, c += GV, item += E::ITEM) {
       copy_wait<DEPTH - 1>();
       if (c < C) {
-        const char* s = ring + slot * slot_bytes;
+        float v[V], xv[SP][V], u[V];
+        kept<V>(item, lane, v);
 #pragma unroll
         for (int i = 0; i < SP; ++i) {
-          if (i < S) {
-            RX::arrived(s + i * G * RX::SLOT, G, l, x + i * p.x_ss + c, xv[i]);
+          if (EXACT || i < S) {
+            RX::arrived(slot + i * RX::SLOT, lane, x + i * p.x_ss + c, xv[i]);
           } else {
 #pragma unroll
             for (int j = 0; j < V; ++j) xv[i][j] = 0.0f;
           }
         }
-      }
-      copy_next();
-      if (++slot == DEPTH) slot = 0;
-      if (c < C) {
-        float u[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) u[j] = 0.0f;
 #pragma unroll
         for (int i = 0; i < SP; ++i) {
-          if (i < S) {
+          if (EXACT || i < S) {
             float o[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) o[j] = b[i] * v[j];
@@ -175,7 +167,7 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
 #pragma unroll
               for (int j = 0; j < V; ++j) o[j] += xv[i][j];
             }
-            RX::store(out + int64_t(i) * C + c, o, C - c);
+            RX::store(out + i * C + c, o, C - c);
             if (p.h) {
 #pragma unroll
               for (int j = 0; j < V; ++j) u[j] += a[i] * RX::round(o[j]);
@@ -185,20 +177,21 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
         if (p.h) {
 #pragma unroll
           for (int j = 0; j < V; ++j) ss[0] += u[j] * u[j];  // past C: y, x and so u are zeros
-          keep<V>(u_s, G, l, k, u);
+          keep<V>(item, lane, u);
         }
       }
+      copy_next();
+      slot = slot == ring + (DEPTH - 1) * E::SLOT ? ring : slot + E::SLOT;
     }
     if (p.h) {
       float total[1];
       GroupSum<1>::run(ss, total, red_next, turn_next, G, group, lane, warp);
       const float r = rsqrtf(of_total(total, 0) * inv_c + p.eps_next);
       TY* h = static_cast<TY*>(p.h) + t * C;
-      for (int k = 0; k < K; ++k) {
-        const int c = (k * G + l) * V;
-        if (c >= C) break;
+      item = item0;
+      for (int c = l * V; c < C; c += GV, item += E::ITEM) {
         float u[V], w[V];
-        kept<V>(u_s, G, l, k, u);
+        kept<V>(item, lane, u);
         p.wn.load<V, ODD>(c, C - c, w);
 #pragma unroll
         for (int j = 0; j < V; ++j) u[j] *= r * w[j];
@@ -214,13 +207,12 @@ namespace {
 struct Forward {
   const Params& p;
   cudaStream_t s;
-  template <int SP, class TX, class TY, int V, bool ODD>
+  template <int SP, bool EXACT, class TX, class TY, int V, bool ODD>
   cudaError_t operator()() const {
-    using E = Leave<SP, TX, TY, V, ODD>;
-    int direct, grid;
-    const Shape sh = fitted(shape_of(p.T, p.C, V, SP == 8 ? 256 : kMaxGroup), false, &direct,
-                            [&](int G, bool) { return E::bytes(p.S, p.C, G); });
-    return launch<leave_kernel<SP, TX, TY, V, ODD>>(p, sh, E::bytes(p.S, p.C, sh.G), 1 << 30, &grid, s);
+    int grid;
+    return launch<leave_kernel<SP, EXACT, TX, TY, V, ODD>>(
+        p, shape_of(p.T, p.C, V, HCB_LEAVE_PER, SP == 8 ? 256 : kMaxGroup), V, Leave<SP, TX, TY, V, ODD>::need,
+        1 << 30, &grid, s);
   }
 };
 

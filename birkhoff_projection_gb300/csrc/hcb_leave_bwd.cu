@@ -5,6 +5,9 @@
 #ifndef HCB_LEAVE_BWD_DEPTH
 #define HCB_LEAVE_BWD_DEPTH 1
 #endif
+#ifndef HCB_LEAVE_BWD_PER
+#define HCB_LEAVE_BWD_PER 2
+#endif
 
 namespace hcb {
 
@@ -26,17 +29,20 @@ struct LeaveBackward {
   using Sum = GroupSum<R>;
   using SumNext = GroupSum<2 * SP>;
   static constexpr int DEPTH = HCB_LEAVE_BWD_DEPTH;
-  static __host__ __device__ constexpr int slot(int S, bool mix, bool gate) {
-    return (mix ? 2 : 1) * S * RX::SLOT + (gate ? 2 : 1) * RY::SLOT;
+  // a slot: dout, y, gate and x; or the stored result, and dh where y would be
+  static constexpr int Y = SP * RX::SLOT, GATE = Y + RY::SLOT, X = GATE + RY::SLOT;
+  __host__ __device__ static constexpr int slot(bool mix, bool gated) {
+    return mix ? X + SP * RX::SLOT : gated ? X : GATE;
   }
-  static size_t bytes(int S, int C, int G, bool mix, bool gate, int weights, bool direct) {
-    const int kept = 4 + (gate ? 4 : 0) + (direct ? 0 : sizeof(TY) + (NEXT ? sizeof(TY) : 0) + 4 * weights);
-    return size_t(G) * (DEPTH * slot(S, mix, gate) + items(C, V, G) * V * kept) +
-           4 * (G / 32 * Co::FLOATS + (Sum::floats(G) + 3) / 4 * 4 + (NEXT ? (SumNext::floats(G) + 3) / 4 * 4 : 0));
-  }
+  // kept: q dv (before it, NEXT: the next block's u); y; NEXT: dh; the shares
+  // of dw and of dw_next; act' w y dv.  direct: the first and the last only.
+  static constexpr int F = kFloats<V>, KY = F, KH = KY + RY::KEPT, KW = KH + (NEXT ? RY::KEPT : 0), KN = KW + F,
+                       KB = KN + (NEXT ? F : 0);
+  __host__ __device__ static constexpr int kb(int direct) { return direct ? F : KB; }
+  __host__ __device__ static constexpr int item(bool gated, int direct) { return kb(direct) + (gated ? F : 0); }
 };
 
-template <int SP, class TX, class TY, int V, bool ODD, bool NEXT>
+template <int SP, bool EXACT, class TX, class TY, int V, bool ODD, bool NEXT>
 __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_kernel(const Params p) {
   using E = LeaveBackward<SP, TX, TY, V, ODD, NEXT>;
   using RX = typename E::RX;
@@ -46,23 +52,19 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
   constexpr int R = E::R, DEPTH = E::DEPTH;
   extern __shared__ __align__(16) char smem[];
   const int G = p.G, NG = blockDim.x / G, group = threadIdx.x / G, l = threadIdx.x % G;
-  const int lane = threadIdx.x & 31, warp = l / 32, C = p.C, S = p.S;
-  const int K = (C + V * G - 1) / (V * G);
+  const int lane = threadIdx.x & 31, warp = l / 32, C = p.C, S = EXACT ? SP : p.S, GV = G * V;
+  const int K = (C + GV - 1) / GV;
   const bool mix = p.P.p != nullptr, gated = p.gate != nullptr;
-  const int slot_bytes = G * E::slot(S, mix, gated);
-  char* ring = smem + size_t(group) * p.group_bytes;
-  float* a_s = reinterpret_cast<float*>(ring + DEPTH * slot_bytes);  // NEXT: u first; then q dv
-  float* b_s = a_s + K * V * G;                                     // act' w y dv
-  char* y_s = reinterpret_cast<char*>(b_s + (gated ? K * V * G : 0));
-  const int row_kept = p.direct ? 0 : K * V * G * static_cast<int>(sizeof(TY));
-  char* dh_s = y_s + row_kept;
-  float* co_all = reinterpret_cast<float*>(dh_s + (NEXT ? row_kept : 0));
+  const int SLOT = E::slot(mix, gated), ITEM = E::item(gated, p.direct), KB = E::kb(p.direct);
+  char* of_group = smem + group * p.group_bytes;
+  char* ring = of_group + warp * p.warp_bytes;
+  char* item0 = ring + DEPTH * SLOT;
+  float* co_all = reinterpret_cast<float*>(of_group + G / 32 * p.warp_bytes);
   float* co_s = co_all + warp * Co::FLOATS;
   float* red = co_all + G / 32 * Co::FLOATS;
-  float* red_next = red + (Sum::floats(G) + 3) / 4 * 4;
-  float* shares = red_next + (NEXT ? (E::SumNext::floats(G) + 3) / 4 * 4 : 0);
-  WeightShare<V> dw = {shares, p.direct ? p.dw + int64_t(blockIdx.x) * pitch(C) : nullptr};
-  WeightShare<V> dwn = {shares + (p.dw ? K * V * G : 0), p.direct ? p.dwn + int64_t(blockIdx.x) * pitch(C) : nullptr};
+  float* red_next = red + Sum::floats(G);
+  float* row_dw = p.direct && p.dw ? p.dw + int64_t(blockIdx.x) * pitch(C) : nullptr;
+  float* row_dwn = NEXT && p.direct && p.dwn ? p.dwn + int64_t(blockIdx.x) * pitch(C) : nullptr;
   int turn = 0, turn_next = 0;
   const float inv_c = 1.0f / static_cast<float>(C);
   const int64_t step = int64_t(gridDim.x) * NG;
@@ -70,83 +72,87 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
 
   const int NI = NEXT ? 2 * K : K;
   int64_t ta = t;
-  int ia = 0, slot_a = 0;
+  int ca = l * V, ia = 0;
+  char* slot_a = ring;
   auto copy_next = [&] {
-    const bool first = NEXT && ia < K;
-    const int c = ((NEXT && !first ? ia - K : ia) * G + l) * V;
-    if (ta < p.T && c < C) {
-      char* s = ring + slot_a * slot_bytes;
-      if (first) {
-        const TX* o = static_cast<const TX*>(p.out_in) + ta * p.out_ts + c;
+    if (ta < p.T && ca < C) {
+      if (NEXT && ia < K) {
+        const TX* o = static_cast<const TX*>(p.out_in) + ta * p.out_ts + ca;
 #pragma unroll
         for (int i = 0; i < SP; ++i)
-          if (i < S) RX::copy(s + i * G * RX::SLOT, G, l, o + i * p.out_ss, C - c);
-        RY::copy(s + S * G * RX::SLOT, G, l, static_cast<const TY*>(p.dh) + ta * p.dh_ts + c, C - c);
+          if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, o + i * p.out_ss, C - ca);
+        RY::copy(slot_a + E::Y, lane, static_cast<const TY*>(p.dh) + ta * p.dh_ts + ca, C - ca);
       } else {
-        const TX* d = static_cast<const TX*>(p.dout) + ta * p.dout_ts + c;
+        const TX* d = static_cast<const TX*>(p.dout) + ta * p.dout_ts + ca;
 #pragma unroll
         for (int i = 0; i < SP; ++i)
-          if (i < S) RX::copy(s + i * G * RX::SLOT, G, l, d + i * p.dout_ss, C - c);
-        s += S * G * RX::SLOT;
-        RY::copy(s, G, l, static_cast<const TY*>(p.y) + ta * p.y_ts + c, C - c);
-        s += G * RY::SLOT;
-        if (gated) {
-          RY::copy(s, G, l, static_cast<const TY*>(p.gate) + ta * p.gate_ts + c, C - c);
-          s += G * RY::SLOT;
-        }
+          if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, d + i * p.dout_ss, C - ca);
+        RY::copy(slot_a + E::Y, lane, static_cast<const TY*>(p.y) + ta * p.y_ts + ca, C - ca);
+        if (gated) RY::copy(slot_a + E::GATE, lane, static_cast<const TY*>(p.gate) + ta * p.gate_ts + ca, C - ca);
         if (mix) {
-          const TX* x = static_cast<const TX*>(p.x) + ta * p.x_ts + c;
+          const TX* x = static_cast<const TX*>(p.x) + ta * p.x_ts + ca;
 #pragma unroll
           for (int i = 0; i < SP; ++i)
-            if (i < S) RX::copy(s + i * G * RX::SLOT, G, l, x + i * p.x_ss, C - c);
+            if (EXACT || i < S) RX::copy(slot_a + E::X + i * RX::SLOT, lane, x + i * p.x_ss, C - ca);
         }
       }
     }
     copy_commit();
-    if (++ia == NI) ia = 0, ta += step;
-    if (++slot_a == DEPTH) slot_a = 0;
+    ca += GV;
+    ++ia;
+    if (NEXT && ia == K) ca = l * V;
+    if (ia == NI) ia = 0, ca = l * V, ta += step;
+    if constexpr (DEPTH > 1) slot_a = slot_a == ring + (DEPTH - 1) * SLOT ? ring : slot_a + SLOT;
   };
   Co co;
   if (t < p.T) co.fetch(p, t, lane);
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) copy_next();
-  if (p.dw) dw.zero(G, l, K, C);
-  if (NEXT && p.dwn) dwn.zero(G, l, K, C);
+  {
+    const float z[V] = {};
+    char* item = item0;
+    for (int c = l * V; c < C; c += GV, item += ITEM) {
+      if (p.direct) {
+        if (row_dw) keep<V, 16>(reinterpret_cast<char*>(row_dw + c), 0, z);
+        if (NEXT && row_dwn) keep<V, 16>(reinterpret_cast<char*>(row_dwn + c), 0, z);
+      } else {
+        keep<V>(item + E::KW, lane, z);
+        if constexpr (NEXT) keep<V>(item + E::KN, lane, z);
+      }
+    }
+  }
 
-  int slot = 0;
+  const char* slot = ring;
   for (; t < p.T; t += step) {
     co.spread(co_s, lane);
     if (t + step < p.T) co.fetch(p, t + step, lane);
     float a[SP], r_next = 0.0f, k_next = 0.0f;
+    const TY* dh = nullptr;
     if constexpr (NEXT) {
       const TX* o = static_cast<const TX*>(p.out_in) + t * p.out_ts;
-      const TY* dh = static_cast<const TY*>(p.dh) + t * p.dh_ts;
+      dh = static_cast<const TY*>(p.dh) + t * p.dh_ts;
       Co::read(co_s, Co::NB, a);
       float sum[2 * SP];
 #pragma unroll
       for (int s = 0; s < 2 * SP; ++s) sum[s] = 0.0f;
-      for (int k = 0; k < K; ++k) {
-        const int c = (k * G + l) * V;
-        float xv[SP][V], g[V], w[V], u[V];
+      char* item = item0;
+      for (int c = l * V, k = 0; k < K; ++k, c += GV, item += ITEM) {
+        float w[V];
         if (c < C) p.wn.load<V, ODD>(c, C - c, w);
         copy_wait<DEPTH - 1>();
         if (c < C) {
-          const char* s = ring + slot * slot_bytes;
+          float xv[SP][V], g[V], u[V];
 #pragma unroll
           for (int i = 0; i < SP; ++i) {
-            if (i < S) {
-              RX::arrived(s + i * G * RX::SLOT, G, l, o + i * p.out_ss + c, xv[i]);
+            if (EXACT || i < S) {
+              RX::arrived(slot + i * RX::SLOT, lane, o + i * p.out_ss + c, xv[i]);
             } else {
 #pragma unroll
               for (int j = 0; j < V; ++j) xv[i][j] = 0.0f;
             }
           }
-          RY::arrived(s + S * G * RX::SLOT, G, l, dh + c, g);
-        }
-        copy_next();
-        if (++slot == DEPTH) slot = 0;
-        if (c < C) {
-          if (!p.direct) keep_row<TY, V>(dh_s, G, l, k, g);
+          RY::arrived(slot + E::Y, lane, dh + c, g);
+          if (!p.direct) RY::keep(item + E::KH, lane, g);
 #pragma unroll
           for (int j = 0; j < V; ++j) {
             g[j] *= w[j];
@@ -159,8 +165,10 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
               sum[SP + s] += u[j] * xv[s][j];
             }
           }
-          keep<V>(a_s, G, l, k, u);
+          keep<V>(item, lane, u);
         }
+        copy_next();
+        if constexpr (DEPTH > 1) slot = slot == ring + (DEPTH - 1) * SLOT ? ring : slot + SLOT;
       }
       float total[1];
       E::SumNext::run(sum, total, red_next, turn_next, G, group, lane, warp);
@@ -189,47 +197,41 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
 #pragma unroll
     for (int i = 0; i < R; ++i) sum[i] = 0.0f;
     TX* dx = p.dx ? static_cast<TX*>(p.dx) + t * S * C : nullptr;
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * G + l) * V;
+    char* item = item0;
+    for (int c = l * V, k = 0; k < K; ++k, c += GV, item += ITEM) {
       float w[V];
       if (c < C) p.w.load<V, ODD>(c, C - c, w);
       copy_wait<DEPTH - 1>();
       if (c >= C) {
         copy_next();
-        if (++slot == DEPTH) slot = 0;
+        if constexpr (DEPTH > 1) slot = slot == ring + (DEPTH - 1) * SLOT ? ring : slot + SLOT;
         continue;
       }
       float D[SP][V], e[V], g[V];
-      const char* s = ring + slot * slot_bytes;
 #pragma unroll
       for (int i = 0; i < SP; ++i) {
-        if (i < S) {
-          RX::arrived(s + i * G * RX::SLOT, G, l, dout + i * p.dout_ss + c, D[i]);
+        if (EXACT || i < S) {
+          RX::arrived(slot + i * RX::SLOT, lane, dout + i * p.dout_ss + c, D[i]);
         } else {
 #pragma unroll
           for (int j = 0; j < V; ++j) D[i][j] = 0.0f;
         }
       }
-      s += S * G * RX::SLOT;
-      RY::arrived(s, G, l, y + c, e);
-      s += G * RY::SLOT;
-      if (gated) {
-        RY::arrived(s, G, l, gate + c, g);
-        s += G * RY::SLOT;
-      }
+      RY::arrived(slot + E::Y, lane, y + c, e);
+      if (gated) RY::arrived(slot + E::GATE, lane, gate + c, g);
       if constexpr (NEXT) {
         float u[V], h[V], wn[V];
-        kept<V>(a_s, G, l, k, u);
+        kept<V>(item, lane, u);
         if (p.direct)
-          RY::load(static_cast<const TY*>(p.dh) + t * p.dh_ts + c, h, C - c);
+          RY::load(dh + c, h, C - c);
         else
-          kept_row<TY, V>(dh_s, G, l, k, h);
+          RY::kept(item + E::KH, lane, h);
         p.wn.load<V, ODD>(c, C - c, wn);
         if (p.dwn) {
           float d[V];
 #pragma unroll
           for (int j = 0; j < V; ++j) d[j] = h[j] * (u[j] * r_next);
-          dwn.add(G, l, k, d);
+          add_share<V>(item + E::KN, lane, row_dwn ? row_dwn + c : nullptr, d);
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -241,9 +243,9 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
       if (mix) {
 #pragma unroll
         for (int q = 0; q < SP; ++q) {
-          if (q < S) {
+          if (EXACT || q < S) {
             float xv[V];
-            RX::arrived(s + q * G * RX::SLOT, G, l, x + q * p.x_ss + c, xv);
+            RX::arrived(slot + E::X + q * RX::SLOT, lane, x + q * p.x_ss + c, xv);
 #pragma unroll
             for (int i = 0; i < SP; ++i)
 #pragma unroll
@@ -252,24 +254,23 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
         }
       }
       copy_next();
-      if (++slot == DEPTH) slot = 0;
+      if constexpr (DEPTH > 1) slot = slot == ring + (DEPTH - 1) * SLOT ? ring : slot + SLOT;
       if (dx) {
 #pragma unroll
         for (int q = 0; q < SP; ++q) {
-          if (q < S) {
-            float d[V];
+          if (EXACT || q < S) {
             if (mix) {
+              float d[V];
 #pragma unroll
               for (int j = 0; j < V; ++j) {
                 d[j] = P[0][q] * D[0][j];
 #pragma unroll
                 for (int i = 1; i < SP; ++i) d[j] += P[i][q] * D[i][j];
               }
+              RX::store(dx + q * C + c, d, C - c);
             } else {
-#pragma unroll
-              for (int j = 0; j < V; ++j) d[j] = D[q][j];
+              RX::store(dx + q * C + c, D[q], C - c);
             }
-            RX::store(dx + int64_t(q) * C + c, d, C - c);
           }
         }
       }
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
 #pragma unroll
         for (int i = 0; i < SP; ++i) dv[j] += b[i] * D[i][j];
       }
-      if (!p.direct) keep_row<TY, V>(y_s, G, l, k, e);
+      if (!p.direct) RY::keep(item + E::KY, lane, e);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         sum[SP * SP + SP] += e[j] * e[j];
@@ -295,9 +296,9 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
           e[j] *= q;
           dv[j] *= q;
         }
-        keep<V>(b_s, G, l, k, g);
+        keep<V>(item + KB, lane, g);
       }
-      keep<V>(a_s, G, l, k, dv);
+      keep<V>(item, lane, dv);
 #pragma unroll
       for (int i = 0; i < SP; ++i)
 #pragma unroll
@@ -325,21 +326,20 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
     }
     TY* dy = p.dy ? static_cast<TY*>(p.dy) + t * C : nullptr;
     TY* dgate = p.dgate ? static_cast<TY*>(p.dgate) + t * C : nullptr;
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * G + l) * V;
-      if (c >= C) break;
+    item = item0;
+    for (int c = l * V; c < C; c += GV, item += ITEM) {
       float yv[V], w[V], d[V];
       if (p.direct)
         RY::load(y + c, yv, C - c);
       else
-        kept_row<TY, V>(y_s, G, l, k, yv);
+        RY::kept(item + E::KY, lane, yv);
       p.w.load<V, ODD>(c, C - c, w);
-      kept<V>(a_s, G, l, k, d);
+      kept<V>(item, lane, d);
 #pragma unroll
       for (int j = 0; j < V; ++j) d[j] *= sr;
       if (dgate) {
         float g[V];
-        kept<V>(b_s, G, l, k, g);
+        kept<V>(item + KB, lane, g);
 #pragma unroll
         for (int j = 0; j < V; ++j) g[j] *= sr;
         RY::store(dgate + c, g, C - c);
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
         float z[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) z[j] = d[j] * yv[j];
-        dw.add(G, l, k, z);
+        add_share<V>(item + E::KW, lane, row_dw ? row_dw + c : nullptr, z);
       }
       if (dy) {
 #pragma unroll
@@ -361,11 +361,9 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
   if (!p.direct && (p.dw || (NEXT && p.dwn))) {
     __syncthreads();
     const int64_t row = int64_t(blockIdx.x) * pitch(C);
-    const size_t back = size_t(group) * p.group_bytes;
-    if (p.dw)
-      sum_shares<V>(reinterpret_cast<float*>(reinterpret_cast<char*>(dw.s) - back), p.group_bytes / 4, G, NG, C, p.dw + row);
-    if (NEXT && p.dwn)
-      sum_shares<V>(reinterpret_cast<float*>(reinterpret_cast<char*>(dwn.s) - back), p.group_bytes / 4, G, NG, C, p.dwn + row);
+    const char* first = smem + DEPTH * SLOT;
+    if (p.dw) sum_shares<V>(first + E::KW, p, G, NG, ITEM, p.dw + row);
+    if (NEXT && p.dwn) sum_shares<V>(first + E::KN, p, G, NG, ITEM, p.dwn + row);
   }
 }
 
@@ -376,16 +374,17 @@ struct Backward {
   const Params& p;
   int* rows;
   cudaStream_t s;
-  template <int SP, class TX, class TY, int V, bool ODD>
+  template <int SP, bool EXACT, class TX, class TY, int V, bool ODD>
   cudaError_t operator()() const {
     using E = LeaveBackward<SP, TX, TY, V, ODD, NEXT>;
-    Params q = p;
-    const int weights = (p.dw != nullptr) + (NEXT && p.dwn != nullptr);
-    const bool mix = p.P.p != nullptr, gate = p.gate != nullptr;
-    const Shape sh = fitted(shape_of(p.T, p.C, V, SP == 8 ? 256 : kMaxGroup), true, &q.direct,
-                            [&](int G, bool direct) { return E::bytes(p.S, p.C, G, mix, gate, weights, direct); });
-    return launch<leave_backward_kernel<SP, TX, TY, V, ODD, NEXT>>(
-        q, sh, E::bytes(p.S, p.C, sh.G, mix, gate, weights, q.direct), weights ? kMaxRows : 1 << 30, rows, s);
+    const bool mix = p.P.p != nullptr, gated = p.gate != nullptr;
+    return launch<leave_backward_kernel<SP, EXACT, TX, TY, V, ODD, NEXT>>(
+        p, shape_of(p.T, p.C, V, HCB_LEAVE_BWD_PER, SP == 8 ? 256 : kMaxGroup), V,
+        [&](int G, int direct) {
+          return Need{E::DEPTH * E::slot(mix, gated), E::item(gated, direct),
+                      4 * (G / 32 * E::Co::FLOATS + E::Sum::floats(G) + (NEXT ? E::SumNext::floats(G) : 0))};
+        },
+        p.dw || p.dwn ? kMaxRows : 1 << 30, rows, s);
   }
 };
 
