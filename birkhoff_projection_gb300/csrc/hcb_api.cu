@@ -24,7 +24,7 @@ bool placed(const void* p, int32_t dtype) { return (reinterpret_cast<uintptr_t>(
 
 // What every entry point asks of sizes and types.
 int check_sizes(const hcb_args* a) {
-  if (a == nullptr || a->T < 0) return B4_EINVAL;
+  if (a == nullptr || a->T < 0 || a->T > INT32_MAX) return B4_EINVAL;
   if (a->S < 1 || a->S > HCB_MAX_STREAMS || a->C < 1 || a->C > HCB_MAX_CHANNELS) return B4_EINVAL;
   for (int32_t d : {a->x_dtype, a->y_dtype, a->w_dtype, a->wn_dtype, a->p_dtype, a->a_dtype, a->b_dtype})
     if (!dtype_ok(d)) return B4_EINVAL;
@@ -32,7 +32,7 @@ int check_sizes(const hcb_args* a) {
   if (a->act < HCB_ACT_NONE || a->act > HCB_ACT_LINEAR) return B4_EINVAL;
   for (int64_t s : {a->x_ts, a->x_ss, a->y_ts, a->gate_ts, a->P_ts, a->a_ts, a->b_ts, a->dout_ts,
                     a->dout_ss, a->dh_ts, a->dres_ts, a->dres_ss, a->out_ts, a->out_ss})
-    if (s < 0) return B4_EINVAL;
+    if (s < 0 || s > INT32_MAX / 4) return B4_EINVAL;
   for (const void* q : {a->x, a->dout, a->dres, a->out_in, static_cast<const void*>(a->out),
                         static_cast<const void*>(a->dx)})
     if (!placed(q, a->x_dtype)) return B4_EINVAL;
@@ -51,15 +51,16 @@ int check_sizes(const hcb_args* a) {
 Params params_of(const hcb_args* a) {
   Params p;
   memset(&p, 0, sizeof(p));
-  p.T = a->T, p.S = a->S, p.C = a->C, p.act = a->act, p.norm = a->norm != 0;
+  p.T = static_cast<uint32_t>(a->T), p.S = a->S, p.C = a->C, p.act = a->act, p.norm = a->norm != 0;
   p.eps = a->eps, p.eps_next = a->eps_next, p.scale = a->scale;
   p.P = {a->P, a->p_dtype == B4_BF16}, p.a = {a->a, a->a_dtype == B4_BF16};
   p.b = {a->b, a->b_dtype == B4_BF16};
   p.w = {a->w, a->w_dtype == B4_BF16}, p.wn = {a->w_next, a->wn_dtype == B4_BF16};
-  p.x_ts = a->x_ts, p.x_ss = a->x_ss, p.y_ts = a->y_ts, p.gate_ts = a->gate_ts;
-  p.P_ts = a->P_ts, p.a_ts = a->a_ts, p.b_ts = a->b_ts;
-  p.dout_ts = a->dout_ts, p.dout_ss = a->dout_ss, p.dh_ts = a->dh_ts;
-  p.dres_ts = a->dres_ts, p.dres_ss = a->dres_ss, p.out_ts = a->out_ts, p.out_ss = a->out_ss;
+  auto u = [](int64_t v) { return static_cast<uint32_t>(v); };
+  p.x_ts = u(a->x_ts), p.x_ss = u(a->x_ss), p.y_ts = u(a->y_ts), p.gate_ts = u(a->gate_ts);
+  p.P_ts = u(a->P_ts), p.a_ts = u(a->a_ts), p.b_ts = u(a->b_ts);
+  p.dout_ts = u(a->dout_ts), p.dout_ss = u(a->dout_ss), p.dh_ts = u(a->dh_ts);
+  p.dres_ts = u(a->dres_ts), p.dres_ss = u(a->dres_ss), p.out_ts = u(a->out_ts), p.out_ss = u(a->out_ss);
   return p;
 }
 
@@ -75,11 +76,11 @@ bool vectors(const hcb_args* a, const Params& p) {
     if (!b4::aligned16(q)) return false;
   const bool x = p.x != nullptr, y = p.y != nullptr, g = p.gate != nullptr, d = p.dout != nullptr;
   const bool h = p.dh != nullptr, r = p.dres != nullptr, o = p.out_in != nullptr, s = p.S > 1;
-  const int64_t strides[] = {x ? p.x_ts : 0,         x && s ? p.x_ss : 0,    y ? p.y_ts : 0,
+  const uint32_t strides[] = {x ? p.x_ts : 0,         x && s ? p.x_ss : 0,    y ? p.y_ts : 0,
                              g ? p.gate_ts : 0,      d ? p.dout_ts : 0,      d && s ? p.dout_ss : 0,
                              h ? p.dh_ts : 0,        r ? p.dres_ts : 0,      r && s ? p.dres_ss : 0,
                              o ? p.out_ts : 0,       o && s ? p.out_ss : 0};
-  for (int64_t v : strides)
+  for (uint32_t v : strides)
     if (v % V != 0) return false;
   return true;
 }

@@ -51,7 +51,7 @@ namespace hcb {
 using b4::bf16_t;
 
 constexpr int kThreads = 256;   // threads of a CTA with many short rows
-constexpr int kMaxGroup = 512;  // threads of a group at most
+constexpr int kMaxGroup = 512;  // threads of a group at most (16 warps: GroupSum)
 constexpr int kMaxRows = 640;   // CTAs of a backward pass at most (rows of partial weight gradients)
 
 // ---------------------------------------------------------------------------
@@ -110,27 +110,18 @@ struct Row {
   // The arrived slot's elements (p: where they came from, for its alignment).
   __device__ __forceinline__ static void arrived(const char* s, int lane, const T* p, float (&v)[V]) {
     uint32_t w[BYTES / 4];
-    if constexpr (ODD) {
-      uint32_t raw[WORDS];
-#pragma unroll
-      for (int i = 0; i < WORDS; ++i) raw[i] = *reinterpret_cast<const uint32_t*>(s + 128 * i + 4 * lane);
-      const uint32_t shift = (reinterpret_cast<uintptr_t>(p) & 3) * 8;
-#pragma unroll
-      for (int i = 0; i < BYTES / 4; ++i)
-        w[i] = sizeof(T) == 4 ? raw[i] : __funnelshift_r(raw[i], raw[i + 1 < WORDS ? i + 1 : i], shift);
-    } else {
-      words(s + lane * BYTES, w);
-    }
+    raw(s, lane, p, w);
     unpack(w, v);
   }
-  // V elements kept in the row's own type (they came from it: exact).
-  __device__ __forceinline__ static void keep(char* s, int lane, const float (&v)[V]) {
+  // The same, and kept as they are at `to`.
+  __device__ __forceinline__ static void arrived_kept(const char* s, int lane, const T* p, float (&v)[V], char* to) {
     uint32_t w[BYTES / 4];
-    pack(v, w);
+    raw(s, lane, p, w);
+    unpack(w, v);
     if constexpr (BYTES == 16)
-      *reinterpret_cast<uint4*>(s + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(to + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     else
-      *reinterpret_cast<uint2*>(s + lane * 8) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(to + lane * 8) = make_uint2(w[0], w[1]);
   }
   __device__ __forceinline__ static void kept(const char* s, int lane, float (&v)[V]) {
     uint32_t w[BYTES / 4];
@@ -197,6 +188,19 @@ struct Row {
   }
 
  private:
+  __device__ __forceinline__ static void raw(const char* s, int lane, const T* p, uint32_t (&w)[BYTES / 4]) {
+    if constexpr (ODD) {
+      uint32_t q[WORDS];
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) q[i] = *reinterpret_cast<const uint32_t*>(s + 128 * i + 4 * lane);
+      const uint32_t shift = (reinterpret_cast<uintptr_t>(p) & 3) * 8;
+#pragma unroll
+      for (int i = 0; i < BYTES / 4; ++i)
+        w[i] = sizeof(T) == 4 ? q[i] : __funnelshift_r(q[i], q[i + 1 < WORDS ? i + 1 : i], shift);
+    } else {
+      words(s + lane * BYTES, w);
+    }
+  }
   __device__ __forceinline__ static void words(const char* s, uint32_t (&w)[BYTES / 4]) {
     if constexpr (BYTES == 16) {
       const uint4 q = *reinterpret_cast<const uint4*>(s);
@@ -307,7 +311,7 @@ __device__ __forceinline__ void put_any(void* p, int32_t bf16, int64_t i, float 
 // Kernel arguments
 // ---------------------------------------------------------------------------
 struct Params {
-  int64_t T;
+  uint32_t T;  // below 2^31, as are the strides: a row's offset is one 32 x 32 -> 64 bit product
   int32_t S, C;
   int32_t G;            // threads of a group
   int32_t group_bytes;  // shared memory of a group
@@ -316,27 +320,39 @@ struct Params {
   float eps, eps_next, scale;
   const void *x, *y, *gate, *dout, *dh, *dres, *out_in;
   Any P, a, b, w, wn;
-  int64_t x_ts, y_ts, gate_ts, P_ts, a_ts, b_ts, dout_ts, dh_ts, dres_ts, out_ts;
-  int64_t x_ss, dout_ss, dres_ss, out_ss;
+  uint32_t x_ts, y_ts, gate_ts, P_ts, a_ts, b_ts, dout_ts, dh_ts, dres_ts, out_ts;
+  uint32_t x_ss, dout_ss, dres_ss, out_ss;
   void *h, *out, *dx, *dy, *dgate, *dP, *da, *db;
   float *dw, *dwn;  // partial weight gradients [CTAs, pitch(C)]
   int32_t direct;   // rows too long to keep all of: the shares lie there from
                     // the start, and y and dh are read a second time
 };
 
+// Row t of an array with `stride` elements between its rows.
+template <class T>
+__device__ __forceinline__ const T* at_row(const void* p, uint32_t t, uint32_t stride) {
+  return static_cast<const T*>(p) + uint64_t(t) * stride;
+}
+
 // Floats of a row of partial weight gradients: whole vectors.
 __host__ __device__ constexpr int pitch(int C) { return (C + 7) / 8 * 8; }
 
-// Write a CTA's sums of its NG groups' shares to its row: item k of warp w of
-// group g keeps them at first + g group_bytes + w warp_bytes + k item.
+// Write a CTA's sums of its NG groups' shares to its row (group 0's threads).
+// `first`: where the first item of this thread's warp is in group 0.
 template <int V>
-__device__ __forceinline__ void sum_shares(const char* first, const Params& p, int G, int NG, int item, float* row) {
-  for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
-    const int vec = c / V, k = vec / G, l = vec % G, e = c % V;
-    const char* at = first + l / 32 * p.warp_bytes + k * item + e / 4 * 512 + l % 32 * 16 + e % 4 * 4;
-    float d = 0.0f;
-    for (int g = 0; g < NG; ++g) d += *reinterpret_cast<const float*>(at + size_t(g) * p.group_bytes);
-    row[c] = d;
+__device__ __forceinline__ void sum_shares(const char* first, const Params& p, int NG, int item, float* row) {
+  if (threadIdx.x >= p.G) return;
+  const int lane = threadIdx.x & 31;
+  for (int c = threadIdx.x * V; c < p.C; c += p.G * V, first += item) {
+    float d[V];
+    kept<V>(first, lane, d);
+    for (int g = 1; g < NG; ++g) {
+      float more[V];
+      kept<V>(first + g * p.group_bytes, lane, more);
+#pragma unroll
+      for (int j = 0; j < V; ++j) d[j] += more[j];
+    }
+    keep<V, 16>(reinterpret_cast<char*>(row + c), 0, d);
   }
 }
 
@@ -351,21 +367,41 @@ struct Coefficients {
   static constexpr int NP = P ? SP * SP : 0, NB = NP + (B ? SP : 0), N = NB + (A ? SP : 0);
   static constexpr int CH = (N + 31) / 32;
   static constexpr int FLOATS = (N + 3) / 4 * 4;
+  // what this lane fetches is the same for every token: an address (or none,
+  // and then a constant), a stride in bytes, a type
+  const char* src[CH];
+  uint32_t stride[CH];
+  bool bf16[CH];
   float next[CH];
-  __device__ __forceinline__ void fetch(const Params& p, int64_t t, int lane) {
+  __device__ __forceinline__ void init(const Params& p, int lane) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int n = c * 32 + lane;
-      float v = 0.0f;
+      src[c] = nullptr, stride[c] = 0, bf16[c] = false, next[c] = 0.0f;
+      const Any* from = nullptr;
+      int at = 0;
       if (n < NP) {
         const int i = n / SP, j = n % SP;
-        if (p.P.p != nullptr && i < p.S && j < p.S) v = p.P.at(t * p.P_ts + i * p.S + j);
+        if (i < p.S && j < p.S) from = p.P.p ? &p.P : nullptr, at = i * p.S + j, stride[c] = p.P_ts;
       } else if (n < NB) {
-        if (n - NP < p.S) v = p.b.p != nullptr ? p.b.at(t * p.b_ts + n - NP) : 1.0f;
+        if (n - NP < p.S) from = &p.b, at = n - NP, stride[c] = p.b_ts;
       } else if (n < N) {
-        if (n - NB < p.S) v = p.a.p != nullptr ? p.a.at(t * p.a_ts + n - NB) : 1.0f;
+        if (n - NB < p.S) from = &p.a, at = n - NB, stride[c] = p.a_ts;
       }
-      next[c] = v;
+      if (from != nullptr) {
+        bf16[c] = from->bf16 != 0;
+        const int size = bf16[c] ? 2 : 4;
+        next[c] = 1.0f;
+        if (from->p != nullptr) src[c] = static_cast<const char*>(from->p) + at * size, stride[c] *= size;
+      }
+    }
+  }
+  __device__ __forceinline__ void fetch(uint32_t t) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if (src[c] == nullptr) continue;
+      const char* q = src[c] + uint64_t(t) * stride[c];
+      next[c] = bf16[c] ? b4::bf16lo(*reinterpret_cast<const uint16_t*>(q)) : *reinterpret_cast<const float*>(q);
     }
   }
   // Put the fetched values where the warp reads them.
@@ -429,28 +465,37 @@ __device__ __forceinline__ float warp_sums(const float (&in)[R], int lane) {
 }
 
 // Sums of R values over a group of G threads: on return lane l of every warp
-// has value l + 32 c in total[c].  `red` holds [2][G / 32][R] floats of the
-// group; `turn` alternates between calls, so that one barrier a call is
-// enough (a warp can be one call ahead of another, not two).
+// has value l + 32 c in total[c].  `red` holds [2][R][20] floats of the group
+// (16 warps at most; 20 keeps the reads of a warp conflict-free), zeros where
+// there are no warps; `turn` alternates between calls, so that one barrier a
+// call is enough (a warp can be one call ahead of another, not two).
 template <int R>
 struct GroupSum {
   static constexpr int CH = (R + 31) / 32;
-  static __host__ __device__ constexpr int floats(int G) { return 2 * (G / 32) * R; }
+  static constexpr __host__ __device__ int floats(int G) { return G == 32 ? 0 : 2 * R * 20; }
+  __device__ __forceinline__ static void clear(float* red, int G, int l) {
+    for (int i = l; i < floats(G); i += G) red[i] = 0.0f;
+  }
   __device__ __forceinline__ static void run(const float (&v)[R], float (&total)[CH], float* red,
                                              int& turn, int G, int group, int lane, int warp) {
     sums<0>(v, total, lane);
     if (G == 32) return;
-    float* r = red + turn * (G / 32) * R;
-    turn ^= 1;
+    float* r = red + turn;
+    turn = R * 20 - turn;
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      if (c * 32 + lane < R) r[warp * R + c * 32 + lane] = total[c];
+      if (c * 32 + lane < R) r[(c * 32 + lane) * 20 + warp] = total[c];
     group_sync(G, group);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       float s = 0.0f;
-      if (c * 32 + lane < R)
-        for (int w = 0; w < G / 32; ++w) s += r[w * R + c * 32 + lane];
+      if (c * 32 + lane < R) {
+        const float4* q = reinterpret_cast<const float4*>(r + (c * 32 + lane) * 20);
+        for (int w = 0; w < G; w += 128) {
+          const float4 x = *q++;
+          s += (x.x + x.y) + (x.z + x.w);
+        }
+      }
       total[c] = s;
     }
   }
@@ -586,7 +631,7 @@ cudaError_t launch(Params p, Shape sh, int V, N&& need, int max_grid, int* grid,
   int occ = 0;
   const cudaError_t e = resident<KERN>(sh.G * sh.NG, smem, &occ);
   if (e != cudaSuccess) return e;
-  const int64_t want = (p.T + sh.NG - 1) / sh.NG;
+  const int64_t want = (int64_t(p.T) + sh.NG - 1) / sh.NG;
   *grid = static_cast<int>(std::min<int64_t>(want, std::min<int64_t>(max_grid, int64_t(sms()) * occ)));
   KERN<<<*grid, sh.G * sh.NG, smem, s>>>(p);
   return cudaGetLastError();

@@ -50,15 +50,17 @@ __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
   float* co_all = reinterpret_cast<float*>(of_group + G / 32 * p.warp_bytes);
   float* co_s = co_all + warp * Co::FLOATS;
   float* red = co_all + G / 32 * Co::FLOATS;
+  E::Sum::clear(red, G, l);
+  group_sync(G, group);
   int turn = 0;
   const float inv_c = 1.0f / static_cast<float>(C);
-  const int64_t step = int64_t(gridDim.x) * NG;
-  int64_t t = int64_t(blockIdx.x) * NG + group;
+  const uint32_t step = gridDim.x * NG;
+  uint32_t t = blockIdx.x * NG + group;
 
-  int64_t ta = t;  // the next item to copy
+  uint32_t ta = t;  // the next item to copy
   int ca = l * V, ka = 0;
   char* slot_a = ring;
-  const TX* xa = static_cast<const TX*>(p.x) + ta * p.x_ts;
+  const TX* xa = at_row<TX>(p.x, ta, p.x_ts);
   auto copy_next = [&] {
     if (ta < p.T && ca < C) {
 #pragma unroll
@@ -67,21 +69,22 @@ __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
     }
     copy_commit();
     ca += GV;
-    if (++ka == K) ka = 0, ca = l * V, ta += step, xa = static_cast<const TX*>(p.x) + ta * p.x_ts;
+    if (++ka == K) ka = 0, ca = l * V, ta += step, xa = at_row<TX>(p.x, ta, p.x_ts);
     slot_a = slot_a == ring + (DEPTH - 1) * E::SLOT ? ring : slot_a + E::SLOT;
   };
   Co co;
-  if (t < p.T) co.fetch(p, t, lane);
+  co.init(p, lane);
+  if (t < p.T) co.fetch(t);
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) copy_next();
 
   const char* slot = ring;
   for (; t < p.T; t += step) {
     co.spread(co_s, lane);
-    if (t + step < p.T) co.fetch(p, t + step, lane);
+    if (t + step < p.T) co.fetch(t + step);
     float a[SP];
     Co::read(co_s, Co::NB, a);
-    const TX* x = static_cast<const TX*>(p.x) + t * p.x_ts;
+    const TX* x = at_row<TX>(p.x, t, p.x_ts);
     float ss[1] = {0.0f};
     char* item = item0;
     for (int c = l * V, k = 0; k < K; ++k, c += GV, item += E::ITEM) {
@@ -109,7 +112,7 @@ __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
     float total[1];
     GroupSum<1>::run(ss, total, red, turn, G, group, lane, warp);
     const float r = rsqrtf(of_total(total, 0) * inv_c + p.eps);
-    TY* h = static_cast<TY*>(p.h) + t * C;
+    TY* h = static_cast<TY*>(p.h) + uint64_t(t) * uint32_t(C);
     item = item0;
     for (int c = l * V; c < C; c += GV, item += E::ITEM) {
       float u[V], w[V];
@@ -162,28 +165,30 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
   float* co_all = reinterpret_cast<float*>(of_group + G / 32 * p.warp_bytes);
   float* co_s = co_all + warp * Co::FLOATS;
   float* red = co_all + G / 32 * Co::FLOATS;
+  Sum::clear(red, G, l);
+  group_sync(G, group);
   float* row_dw = p.direct && p.dw ? p.dw + int64_t(blockIdx.x) * pitch(C) : nullptr;
   int turn = 0;
   const float inv_c = 1.0f / static_cast<float>(C);
-  const int64_t step = int64_t(gridDim.x) * NG;
-  int64_t t = int64_t(blockIdx.x) * NG + group;
+  const uint32_t step = gridDim.x * NG;
+  uint32_t t = blockIdx.x * NG + group;
 
   // items of a token: x and dh for every k, then, if there is one, dres
   const int NI = p.dres ? 2 * K : K;
-  int64_t ta = t;
+  uint32_t ta = t;
   int ca = l * V, ia = 0;
   char* slot_a = ring;
   auto copy_next = [&] {
     const bool second = ia >= K;
     if (ta < p.T && ca < C) {
-      const TX* x = second ? static_cast<const TX*>(p.dres) + ta * p.dres_ts
-                           : static_cast<const TX*>(p.x) + ta * p.x_ts;
+      const TX* x = second ? at_row<TX>(p.dres, ta, p.dres_ts)
+                           : at_row<TX>(p.x, ta, p.x_ts);
       const int64_t ss = second ? p.dres_ss : p.x_ss;
 #pragma unroll
       for (int i = 0; i < SP; ++i)
         if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, x + i * ss + ca, C - ca);
       if (!second)
-        RY::copy(slot_a + E::DH, lane, static_cast<const TY*>(p.dh) + ta * p.dh_ts + ca, C - ca);
+        RY::copy(slot_a + E::DH, lane, at_row<TY>(p.dh, ta, p.dh_ts) + ca, C - ca);
     }
     copy_commit();
     ca += GV;
@@ -193,7 +198,8 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
     slot_a = slot_a == ring + (DEPTH - 1) * E::SLOT ? ring : slot_a + E::SLOT;
   };
   Co co;
-  if (t < p.T) co.fetch(p, t, lane);
+  co.init(p, lane);
+  if (t < p.T) co.fetch(t);
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) copy_next();
   if (p.dw) {
@@ -210,11 +216,11 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
   const char* slot = ring;
   for (; t < p.T; t += step) {
     co.spread(co_s, lane);
-    if (t + step < p.T) co.fetch(p, t + step, lane);
+    if (t + step < p.T) co.fetch(t + step);
     float a[SP];
     Co::read(co_s, Co::NB, a);
-    const TX* x = static_cast<const TX*>(p.x) + t * p.x_ts;
-    const TY* dh = static_cast<const TY*>(p.dh) + t * p.dh_ts;
+    const TX* x = at_row<TX>(p.x, t, p.x_ts);
+    const TY* dh = at_row<TY>(p.dh, t, p.dh_ts);
     float sum[2 * SP];
 #pragma unroll
     for (int s = 0; s < 2 * SP; ++s) sum[s] = 0.0f;
@@ -234,8 +240,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
             for (int j = 0; j < V; ++j) xv[i][j] = 0.0f;
           }
         }
-        RY::arrived(slot + E::DH, lane, dh + c, g);
-        RY::keep(item + E::KH, lane, g);
+        RY::arrived_kept(slot + E::DH, lane, dh + c, g, item + E::KH);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           g[j] *= w[j];
@@ -265,10 +270,10 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
     const float k_u = gu * inv_c * r * r;
     if (p.da) {
       const float u_x = __shfl_sync(0xffffffffu, total[0], (lane + SP) & 31);
-      if (warp == 0 && lane < S) put_any(p.da, p.a.bf16, t * S + lane, r * (total[0] - k_u * u_x));
+      if (warp == 0 && lane < S) put_any(p.da, p.a.bf16, int64_t(t) * S + lane, r * (total[0] - k_u * u_x));
     }
-    const TX* dres = p.dres ? static_cast<const TX*>(p.dres) + t * p.dres_ts : nullptr;
-    TX* dx = p.dx ? static_cast<TX*>(p.dx) + t * S * C : nullptr;
+    const TX* dres = p.dres ? at_row<TX>(p.dres, t, p.dres_ts) : nullptr;
+    TX* dx = p.dx ? static_cast<TX*>(p.dx) + uint64_t(t) * uint32_t(S * C) : nullptr;
     item = item0;
     for (int c = l * V, k = 0; k < K; ++k, c += GV, item += ITEM) {
       if (dres) copy_wait<DEPTH - 1>();
@@ -312,7 +317,8 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
   copy_wait_all();
   if (p.dw && !p.direct) {
     __syncthreads();
-    sum_shares<V>(smem + DEPTH * E::SLOT + E::KW, p, G, NG, ITEM, p.dw + int64_t(blockIdx.x) * pitch(C));
+    sum_shares<V>(smem + warp * p.warp_bytes + DEPTH * E::SLOT + E::KW, p, NG, ITEM,
+                  p.dw + int64_t(blockIdx.x) * pitch(C));
   }
 }
 

@@ -50,25 +50,28 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
   float* co_s = co_all + warp * Co::FLOATS;
   float* red = co_all + G / 32 * Co::FLOATS;
   float* red_next = red + GroupSum<1>::floats(G);
+  E::Sum::clear(red, G, l);
+  E::Sum::clear(red_next, G, l);
+  group_sync(G, group);
   int turn = 0, turn_next = 0;
   const float inv_c = 1.0f / static_cast<float>(C);
   const bool mix = p.P.p != nullptr, gated = p.gate != nullptr;
-  const int64_t step = int64_t(gridDim.x) * NG;
-  int64_t t = int64_t(blockIdx.x) * NG + group;
+  const uint32_t step = gridDim.x * NG;
+  uint32_t t = blockIdx.x * NG + group;
 
-  int64_t ta = t;
+  uint32_t ta = t;
   int ca = l * V, ia = 0;
   char* slot_a = ring;
   auto copy_next = [&] {
     if (ta < p.T && ca < C) {
       if (ia >= K) {
-        const TX* x = static_cast<const TX*>(p.x) + ta * p.x_ts + ca;
+        const TX* x = at_row<TX>(p.x, ta, p.x_ts) + ca;
 #pragma unroll
         for (int i = 0; i < SP; ++i)
           if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, x + i * p.x_ss, C - ca);
       } else {
-        RY::copy(slot_a + E::Y, lane, static_cast<const TY*>(p.y) + ta * p.y_ts + ca, C - ca);
-        if (gated) RY::copy(slot_a + E::Y + RY::SLOT, lane, static_cast<const TY*>(p.gate) + ta * p.gate_ts + ca, C - ca);
+        RY::copy(slot_a + E::Y, lane, at_row<TY>(p.y, ta, p.y_ts) + ca, C - ca);
+        if (gated) RY::copy(slot_a + E::Y + RY::SLOT, lane, at_row<TY>(p.gate, ta, p.gate_ts) + ca, C - ca);
       }
     }
     copy_commit();
@@ -79,17 +82,18 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
     slot_a = slot_a == ring + (DEPTH - 1) * E::SLOT ? ring : slot_a + E::SLOT;
   };
   Co co;
-  if (t < p.T) co.fetch(p, t, lane);
+  co.init(p, lane);
+  if (t < p.T) co.fetch(t);
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) copy_next();
 
   const char* slot = ring;
   for (; t < p.T; t += step) {
     co.spread(co_s, lane);
-    if (t + step < p.T) co.fetch(p, t + step, lane);
-    const TX* x = static_cast<const TX*>(p.x) + t * p.x_ts;
-    const TY* y = static_cast<const TY*>(p.y) + t * p.y_ts;
-    const TY* gate = static_cast<const TY*>(p.gate) + t * p.gate_ts;
+    if (t + step < p.T) co.fetch(t + step);
+    const TX* x = at_row<TX>(p.x, t, p.x_ts);
+    const TY* y = at_row<TY>(p.y, t, p.y_ts);
+    const TY* gate = at_row<TY>(p.gate, t, p.gate_ts);
     float ss[1] = {0.0f};
     char* item = item0;
     for (int c = l * V, k = 0; k < K; ++k, c += GV, item += E::ITEM) {
@@ -133,7 +137,7 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
       Co::read(co_s, i * SP, P[i]);
       b[i] *= rho;
     }
-    TX* out = static_cast<TX*>(p.out) + t * S * C;
+    TX* out = static_cast<TX*>(p.out) + uint64_t(t) * uint32_t(S * C);
     ss[0] = 0.0f;
     item = item0;
     for (int c = l * V, k = 0; k < K; ++k, c += GV, item += E::ITEM) {
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
       float total[1];
       GroupSum<1>::run(ss, total, red_next, turn_next, G, group, lane, warp);
       const float r = rsqrtf(of_total(total, 0) * inv_c + p.eps_next);
-      TY* h = static_cast<TY*>(p.h) + t * C;
+      TY* h = static_cast<TY*>(p.h) + uint64_t(t) * uint32_t(C);
       item = item0;
       for (int c = l * V; c < C; c += GV, item += E::ITEM) {
         float u[V], w[V];

@@ -63,34 +63,37 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
   float* co_s = co_all + warp * Co::FLOATS;
   float* red = co_all + G / 32 * Co::FLOATS;
   float* red_next = red + Sum::floats(G);
+  Sum::clear(red, G, l);
+  if constexpr (NEXT) E::SumNext::clear(red_next, G, l);
+  group_sync(G, group);
   float* row_dw = p.direct && p.dw ? p.dw + int64_t(blockIdx.x) * pitch(C) : nullptr;
   float* row_dwn = NEXT && p.direct && p.dwn ? p.dwn + int64_t(blockIdx.x) * pitch(C) : nullptr;
   int turn = 0, turn_next = 0;
   const float inv_c = 1.0f / static_cast<float>(C);
-  const int64_t step = int64_t(gridDim.x) * NG;
-  int64_t t = int64_t(blockIdx.x) * NG + group;
+  const uint32_t step = gridDim.x * NG;
+  uint32_t t = blockIdx.x * NG + group;
 
   const int NI = NEXT ? 2 * K : K;
-  int64_t ta = t;
+  uint32_t ta = t;
   int ca = l * V, ia = 0;
   char* slot_a = ring;
   auto copy_next = [&] {
     if (ta < p.T && ca < C) {
       if (NEXT && ia < K) {
-        const TX* o = static_cast<const TX*>(p.out_in) + ta * p.out_ts + ca;
+        const TX* o = at_row<TX>(p.out_in, ta, p.out_ts) + ca;
 #pragma unroll
         for (int i = 0; i < SP; ++i)
           if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, o + i * p.out_ss, C - ca);
-        RY::copy(slot_a + E::Y, lane, static_cast<const TY*>(p.dh) + ta * p.dh_ts + ca, C - ca);
+        RY::copy(slot_a + E::Y, lane, at_row<TY>(p.dh, ta, p.dh_ts) + ca, C - ca);
       } else {
-        const TX* d = static_cast<const TX*>(p.dout) + ta * p.dout_ts + ca;
+        const TX* d = at_row<TX>(p.dout, ta, p.dout_ts) + ca;
 #pragma unroll
         for (int i = 0; i < SP; ++i)
           if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, d + i * p.dout_ss, C - ca);
-        RY::copy(slot_a + E::Y, lane, static_cast<const TY*>(p.y) + ta * p.y_ts + ca, C - ca);
-        if (gated) RY::copy(slot_a + E::GATE, lane, static_cast<const TY*>(p.gate) + ta * p.gate_ts + ca, C - ca);
+        RY::copy(slot_a + E::Y, lane, at_row<TY>(p.y, ta, p.y_ts) + ca, C - ca);
+        if (gated) RY::copy(slot_a + E::GATE, lane, at_row<TY>(p.gate, ta, p.gate_ts) + ca, C - ca);
         if (mix) {
-          const TX* x = static_cast<const TX*>(p.x) + ta * p.x_ts + ca;
+          const TX* x = at_row<TX>(p.x, ta, p.x_ts) + ca;
 #pragma unroll
           for (int i = 0; i < SP; ++i)
             if (EXACT || i < S) RX::copy(slot_a + E::X + i * RX::SLOT, lane, x + i * p.x_ss, C - ca);
@@ -105,7 +108,8 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
     if constexpr (DEPTH > 1) slot_a = slot_a == ring + (DEPTH - 1) * SLOT ? ring : slot_a + SLOT;
   };
   Co co;
-  if (t < p.T) co.fetch(p, t, lane);
+  co.init(p, lane);
+  if (t < p.T) co.fetch(t);
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) copy_next();
   {
@@ -125,12 +129,12 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
   const char* slot = ring;
   for (; t < p.T; t += step) {
     co.spread(co_s, lane);
-    if (t + step < p.T) co.fetch(p, t + step, lane);
+    if (t + step < p.T) co.fetch(t + step);
     float a[SP], r_next = 0.0f, k_next = 0.0f;
     const TY* dh = nullptr;
     if constexpr (NEXT) {
-      const TX* o = static_cast<const TX*>(p.out_in) + t * p.out_ts;
-      dh = static_cast<const TY*>(p.dh) + t * p.dh_ts;
+      const TX* o = at_row<TX>(p.out_in, t, p.out_ts);
+      dh = at_row<TY>(p.dh, t, p.dh_ts);
       Co::read(co_s, Co::NB, a);
       float sum[2 * SP];
 #pragma unroll
@@ -151,8 +155,10 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
               for (int j = 0; j < V; ++j) xv[i][j] = 0.0f;
             }
           }
-          RY::arrived(slot + E::Y, lane, dh + c, g);
-          if (!p.direct) RY::keep(item + E::KH, lane, g);
+          if (p.direct)
+            RY::arrived(slot + E::Y, lane, dh + c, g);
+          else
+            RY::arrived_kept(slot + E::Y, lane, dh + c, g, item + E::KH);
 #pragma unroll
           for (int j = 0; j < V; ++j) {
             g[j] *= w[j];
@@ -183,20 +189,20 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
       if (p.da) {
         const float u_x = __shfl_sync(0xffffffffu, total[0], (lane + SP) & 31);
         if (warp == 0 && lane < S)
-          put_any(p.da, p.a.bf16, t * S + lane, r_next * (total[0] - k_next * u_x));
+          put_any(p.da, p.a.bf16, int64_t(t) * S + lane, r_next * (total[0] - k_next * u_x));
       }
     }
-    const TX* dout = static_cast<const TX*>(p.dout) + t * p.dout_ts;
-    const TX* x = static_cast<const TX*>(p.x) + t * p.x_ts;
-    const TY* y = static_cast<const TY*>(p.y) + t * p.y_ts;
-    const TY* gate = static_cast<const TY*>(p.gate) + t * p.gate_ts;
+    const TX* dout = at_row<TX>(p.dout, t, p.dout_ts);
+    const TX* x = at_row<TX>(p.x, t, p.x_ts);
+    const TY* y = at_row<TY>(p.y, t, p.y_ts);
+    const TY* gate = at_row<TY>(p.gate, t, p.gate_ts);
     float P[SP][SP], b[SP], sum[R];
     Co::read(co_s, Co::NP, b);
 #pragma unroll
     for (int i = 0; i < SP; ++i) Co::read(co_s, i * SP, P[i]);
 #pragma unroll
     for (int i = 0; i < R; ++i) sum[i] = 0.0f;
-    TX* dx = p.dx ? static_cast<TX*>(p.dx) + t * S * C : nullptr;
+    TX* dx = p.dx ? static_cast<TX*>(p.dx) + uint64_t(t) * uint32_t(S * C) : nullptr;
     char* item = item0;
     for (int c = l * V, k = 0; k < K; ++k, c += GV, item += ITEM) {
       float w[V];
@@ -217,7 +223,10 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
           for (int j = 0; j < V; ++j) D[i][j] = 0.0f;
         }
       }
-      RY::arrived(slot + E::Y, lane, y + c, e);
+      if (p.direct)
+        RY::arrived(slot + E::Y, lane, y + c, e);
+      else
+        RY::arrived_kept(slot + E::Y, lane, y + c, e, item + E::KY);
       if (gated) RY::arrived(slot + E::GATE, lane, gate + c, g);
       if constexpr (NEXT) {
         float u[V], h[V], wn[V];
@@ -281,7 +290,6 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
 #pragma unroll
         for (int i = 0; i < SP; ++i) dv[j] += b[i] * D[i][j];
       }
-      if (!p.direct) RY::keep(item + E::KY, lane, e);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         sum[SP * SP + SP] += e[j] * e[j];
@@ -318,14 +326,14 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
         const int i = ch * 32 + lane;
         if (i < SP * SP) {
           if (p.dP && i / SP < S && i % SP < S)
-            put_any(p.dP, p.P.bf16, (t * S + i / SP) * S + i % SP, total[ch]);
+            put_any(p.dP, p.P.bf16, (int64_t(t) * S + i / SP) * S + i % SP, total[ch]);
         } else if (i < SP * SP + S) {
-          if (p.db) put_any(p.db, p.b.bf16, t * S + i - SP * SP, sr * total[ch]);
+          if (p.db) put_any(p.db, p.b.bf16, int64_t(t) * S + i - SP * SP, sr * total[ch]);
         }
       }
     }
-    TY* dy = p.dy ? static_cast<TY*>(p.dy) + t * C : nullptr;
-    TY* dgate = p.dgate ? static_cast<TY*>(p.dgate) + t * C : nullptr;
+    TY* dy = p.dy ? static_cast<TY*>(p.dy) + uint64_t(t) * uint32_t(C) : nullptr;
+    TY* dgate = p.dgate ? static_cast<TY*>(p.dgate) + uint64_t(t) * uint32_t(C) : nullptr;
     item = item0;
     for (int c = l * V; c < C; c += GV, item += ITEM) {
       float yv[V], w[V], d[V];
@@ -361,9 +369,9 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_backward_k
   if (!p.direct && (p.dw || (NEXT && p.dwn))) {
     __syncthreads();
     const int64_t row = int64_t(blockIdx.x) * pitch(C);
-    const char* first = smem + DEPTH * SLOT;
-    if (p.dw) sum_shares<V>(first + E::KW, p, G, NG, ITEM, p.dw + row);
-    if (NEXT && p.dwn) sum_shares<V>(first + E::KN, p, G, NG, ITEM, p.dwn + row);
+    const char* first = smem + warp * p.warp_bytes + DEPTH * SLOT;
+    if (p.dw) sum_shares<V>(first + E::KW, p, NG, ITEM, p.dw + row);
+    if (NEXT && p.dwn) sum_shares<V>(first + E::KN, p, NG, ITEM, p.dwn + row);
   }
 }
 

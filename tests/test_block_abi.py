@@ -91,7 +91,7 @@ def call(L, name, **kw):
 
 @pytest.mark.parametrize("name", sorted(ENTRIES))
 def test_block_entries_refuse_bad_sizes_and_types(L, name):
-    bad = [dict(T=-1), dict(S=0), dict(S=9), dict(C=0), dict(C=16385), dict(x_dtype=2), dict(y_dtype=-1),
+    bad = [dict(T=-1), dict(T=2**31), dict(x_ts=2**29), dict(b_ts=2**40), dict(S=0), dict(S=9), dict(C=0), dict(C=16385), dict(x_dtype=2), dict(y_dtype=-1),
            dict(w_dtype=5), dict(wn_dtype=2), dict(p_dtype=2), dict(a_dtype=2), dict(b_dtype=2), dict(eps=-1.0),
            dict(eps=float("nan")), dict(eps=float("inf")), dict(eps_next=-1.0), dict(scale=float("inf")),
            dict(scale=float("nan")), dict(act=4), dict(act=-1), dict(x_ts=-1), dict(x_ss=-4), dict(y_ts=-1),
