@@ -229,7 +229,8 @@ int hcb_leave_backward(const hcb_args* a, birkhoff4_stream_t stream) {
     p.wn.p = nullptr;
   }
   int rows = 0;
-  cudaError_t e = leave_backward(p, a->x_dtype == B4_BF16, a->y_dtype == B4_BF16, vectors(a, p), &rows, s);
+  cudaError_t e = (next ? leave_enter_backward : leave_backward)(p, a->x_dtype == B4_BF16, a->y_dtype == B4_BF16,
+                                                                vectors(a, p), &rows, s);
   if (e == cudaSuccess) e = finish(a, p, rows, s);
   return b4::record_cuda_error(e);
 }

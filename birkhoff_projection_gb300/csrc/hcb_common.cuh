@@ -64,6 +64,45 @@ constexpr int kMaxRows = 640;   // CTAs of a backward pass at most (rows of part
 // whole; no allocation begins inside a word.  Past the row's last element
 // nothing is read (the copy's source size) and the slot holds zeros.
 // ---------------------------------------------------------------------------
+// Two floats of neighbouring channels, for the packed fp32 instructions
+// (fma.rn.f32x2 and so on: the same roundings as one by one, half the issue
+// slots; the kernels are near the issue limit).
+using P2 = unsigned long long;
+__device__ __forceinline__ P2 pair(float lo, float hi) {
+  P2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ P2 twice(float x) { return pair(x, x); }
+__device__ __forceinline__ void split(P2 x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ float low(P2 x) {
+  float lo, hi;
+  split(x, lo, hi);
+  return lo;
+}
+__device__ __forceinline__ float both(P2 x) {  // their sum
+  float lo, hi;
+  split(x, lo, hi);
+  return lo + hi;
+}
+__device__ __forceinline__ P2 fma2(P2 a, P2 b, P2 c) {
+  P2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ P2 mul2(P2 a, P2 b) {
+  P2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ P2 add2(P2 a, P2 b) {
+  P2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -73,6 +112,7 @@ __device__ __forceinline__ void copy_wait() {
 
 template <class T, int V, bool ODD>
 struct Row {
+  static constexpr int H = V / 2;
   static constexpr int BYTES = V * static_cast<int>(sizeof(T));
   static constexpr int WORDS = BYTES / 4 + (ODD && sizeof(T) == 2 ? 1 : 0);
   static constexpr int SLOT = 32 * 4 * WORDS;  // bytes of a warp in a slot
@@ -108,13 +148,13 @@ struct Row {
     }
   }
   // The arrived slot's elements (p: where they came from, for its alignment).
-  __device__ __forceinline__ static void arrived(const char* s, int lane, const T* p, float (&v)[V]) {
+  __device__ __forceinline__ static void arrived(const char* s, int lane, const T* p, P2 (&v)[H]) {
     uint32_t w[BYTES / 4];
     raw(s, lane, p, w);
     unpack(w, v);
   }
   // The same, and kept as they are at `to`.
-  __device__ __forceinline__ static void arrived_kept(const char* s, int lane, const T* p, float (&v)[V], char* to) {
+  __device__ __forceinline__ static void arrived_kept(const char* s, int lane, const T* p, P2 (&v)[H], char* to) {
     uint32_t w[BYTES / 4];
     raw(s, lane, p, w);
     unpack(w, v);
@@ -123,68 +163,44 @@ struct Row {
     else
       *reinterpret_cast<uint2*>(to + lane * 8) = make_uint2(w[0], w[1]);
   }
-  __device__ __forceinline__ static void kept(const char* s, int lane, float (&v)[V]) {
+  __device__ __forceinline__ static void kept(const char* s, int lane, P2 (&v)[H]) {
     uint32_t w[BYTES / 4];
     words(s + lane * BYTES, w);
     unpack(w, v);
   }
   // p[0, min(V, left)) read directly, zeros behind.
-  __device__ __forceinline__ static void load(const T* p, float (&v)[V], int left) {
+  __device__ __forceinline__ static void load(const T* p, P2 (&v)[H], int left) {
     if constexpr (ODD) {
+      float x[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        v[i] = 0.0f;
+        x[i] = 0.0f;
         if (i < left) {
           if constexpr (sizeof(T) == 4)
-            v[i] = p[i];
+            x[i] = p[i];
           else
-            v[i] = b4::bf16lo(p[i].bits);
+            x[i] = b4::bf16lo(p[i].bits);
         }
       }
+#pragma unroll
+      for (int i = 0; i < H; ++i) v[i] = pair(x[2 * i], x[2 * i + 1]);
     } else {
       uint32_t w[BYTES / 4];
-#pragma unroll
-      for (int i = 0; i < BYTES / 8; ++i) {
-        const uint2 q = reinterpret_cast<const uint2*>(p)[i];
-        w[2 * i] = q.x, w[2 * i + 1] = q.y;
-      }
+      words(reinterpret_cast<const char*>(p), w);
       unpack(w, v);
     }
   }
-  // Round and write v to p[0, min(V, left)).
-  __device__ __forceinline__ static void store(T* p, const float (&v)[V], int left) {
+  // Round and write v to p[0, min(V, left)); v becomes what was written.
+  __device__ __forceinline__ static void store_rounded(T* p, P2 (&v)[H], int left) {
     uint32_t w[BYTES / 4];
     pack(v, w);
-    if constexpr (!ODD) {
-      if constexpr (BYTES == 16)
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-      else
-        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i < left) p[i] = v[i];
-    } else {
-      uint16_t* e = reinterpret_cast<uint16_t*>(p);
-      if (left < V) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (i < left) e[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
-      } else if ((reinterpret_cast<uintptr_t>(p) & 3) == 0) {
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) reinterpret_cast<uint32_t*>(p)[i] = w[i];
-      } else {
-        e[0] = static_cast<uint16_t>(w[0]);
-#pragma unroll
-        for (int i = 0; i < V / 2 - 1; ++i)
-          reinterpret_cast<uint32_t*>(e + 1)[i] = __funnelshift_r(w[i], w[i + 1], 16);
-        e[V - 1] = static_cast<uint16_t>(w[V / 2 - 1] >> 16);
-      }
-    }
+    put(p, w, left);
+    if constexpr (sizeof(T) == 2) unpack(w, v);
   }
-  __device__ __forceinline__ static float round(float x) {
-    if constexpr (sizeof(T) == 4) return x;
-    return b4::bf16lo(b4::pack_bf16(x, 0.0f));
+  __device__ __forceinline__ static void store(T* p, const P2 (&v)[H], int left) {
+    uint32_t w[BYTES / 4];
+    pack(v, w);
+    put(p, w, left);
   }
 
  private:
@@ -210,22 +226,49 @@ struct Row {
       w[0] = q.x, w[1] = q.y;
     }
   }
-  __device__ __forceinline__ static void unpack(const uint32_t (&w)[BYTES / 4], float (&v)[V]) {
-    if constexpr (sizeof(T) == 4) {
+  __device__ __forceinline__ static void unpack(const uint32_t (&w)[BYTES / 4], P2 (&v)[H]) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = __uint_as_float(w[i]);
-    } else {
+    for (int i = 0; i < H; ++i)
+      v[i] = sizeof(T) == 4 ? pair(__uint_as_float(w[(2 * i) % (BYTES / 4)]), __uint_as_float(w[(2 * i + 1) % (BYTES / 4)]))
+                            : pair(b4::bf16lo(w[i]), b4::bf16hi(w[i]));
+  }
+  __device__ __forceinline__ static void pack(const P2 (&v)[H], uint32_t (&w)[BYTES / 4]) {
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i) v[2 * i] = b4::bf16lo(w[i]), v[2 * i + 1] = b4::bf16hi(w[i]);
+    for (int i = 0; i < H; ++i) {
+      float lo, hi;
+      split(v[i], lo, hi);
+      if constexpr (sizeof(T) == 4)
+        w[2 * i] = __float_as_uint(lo), w[2 * i + 1] = __float_as_uint(hi);
+      else
+        w[i] = b4::pack_bf16(lo, hi);
     }
   }
-  __device__ __forceinline__ static void pack(const float (&v)[V], uint32_t (&w)[BYTES / 4]) {
-    if constexpr (sizeof(T) == 4) {
+  __device__ __forceinline__ static void put(T* p, const uint32_t (&w)[BYTES / 4], int left) {
+    if constexpr (!ODD) {
+      if constexpr (BYTES == 16)
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+      else
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) w[i] = __float_as_uint(v[i]);
+      for (int i = 0; i < V; ++i)
+        if (i < left) p[i] = __uint_as_float(w[i]);
     } else {
+      uint16_t* e = reinterpret_cast<uint16_t*>(p);
+      if (left < V) {
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i) w[i] = b4::pack_bf16(v[2 * i], v[2 * i + 1]);
+        for (int i = 0; i < V; ++i)
+          if (i < left) e[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+      } else if ((reinterpret_cast<uintptr_t>(p) & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+      } else {
+        e[0] = static_cast<uint16_t>(w[0]);
+#pragma unroll
+        for (int i = 0; i < H - 1; ++i)
+          reinterpret_cast<uint32_t*>(e + 1)[i] = __funnelshift_r(w[i], w[i + 1], 16);
+        e[V - 1] = static_cast<uint16_t>(w[H - 1] >> 16);
+      }
     }
   }
 };
@@ -234,35 +277,35 @@ struct Row {
 template <int V>
 constexpr int kFloats = 128 * V;  // bytes of a warp
 template <int V, int PLANE = 512>
-__device__ __forceinline__ void keep(char* s, int lane, const float (&v)[V]) {
+__device__ __forceinline__ void keep(char* s, int lane, const P2 (&v)[V / 2]) {
 #pragma unroll
   for (int i = 0; i < V / 4; ++i)
-    *reinterpret_cast<float4*>(s + lane * 16 + i * PLANE) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    *reinterpret_cast<ulonglong2*>(s + lane * 16 + i * PLANE) = make_ulonglong2(v[2 * i], v[2 * i + 1]);
 }
 template <int V, int PLANE = 512>
-__device__ __forceinline__ void kept(const char* s, int lane, float (&v)[V]) {
+__device__ __forceinline__ void kept(const char* s, int lane, P2 (&v)[V / 2]) {
 #pragma unroll
   for (int i = 0; i < V / 4; ++i) {
-    const float4 q = *reinterpret_cast<const float4*>(s + lane * 16 + i * PLANE);
-    v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
+    const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(s + lane * 16 + i * PLANE);
+    v[2 * i] = q.x, v[2 * i + 1] = q.y;
   }
 }
 
-// Add v to a thread's share of a weight gradient: in shared memory at s, or,
-// where rows are too long for that, in the group's row of the partial sums
-// (global memory that only this thread touches; such groups are CTAs).
+// Add a b to a thread's share of a weight gradient: in shared memory at s,
+// or, where rows are too long for that, in the group's row of the partial
+// sums (global memory that only this thread touches; such groups are CTAs).
 template <int V>
-__device__ __forceinline__ void add_share(char* s, int lane, float* g, const float (&v)[V]) {
-  float d[V];
+__device__ __forceinline__ void add_share(char* s, int lane, float* g, const P2 (&a)[V / 2], const P2 (&b)[V / 2]) {
+  P2 d[V / 2];
   if (g == nullptr) {
     kept<V>(s, lane, d);
 #pragma unroll
-    for (int i = 0; i < V; ++i) d[i] += v[i];
+    for (int i = 0; i < V / 2; ++i) d[i] = fma2(a[i], b[i], d[i]);
     keep<V>(s, lane, d);
   } else {
     kept<V, 16>(reinterpret_cast<const char*>(g), 0, d);
 #pragma unroll
-    for (int i = 0; i < V; ++i) d[i] += v[i];
+    for (int i = 0; i < V / 2; ++i) d[i] = fma2(a[i], b[i], d[i]);
     keep<V, 16>(reinterpret_cast<char*>(g), 0, d);
   }
 }
@@ -277,24 +320,25 @@ struct Any {
   }
   // Elements [i, i + V), 1 where there are none (left: elements from i on).
   template <int V, bool ODD>
-  __device__ __forceinline__ void load(int i, int left, float (&v)[V]) const {
+  __device__ __forceinline__ void load(int i, int left, P2 (&v)[V / 2]) const {
     if (p == nullptr) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) v[k] = 1.0f;
+      for (int k = 0; k < V / 2; ++k) v[k] = twice(1.0f);
     } else if constexpr (ODD) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) v[k] = k < left ? at(i + k) : 0.0f;
+      for (int k = 0; k < V / 2; ++k)
+        v[k] = pair(2 * k < left ? at(i + 2 * k) : 0.0f, 2 * k + 1 < left ? at(i + 2 * k + 1) : 0.0f);
     } else if (bf16) {
 #pragma unroll
-      for (int k = 0; k < V; k += 4) {
-        const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i + k);
-        v[k] = b4::bf16lo(q.x), v[k + 1] = b4::bf16hi(q.x), v[k + 2] = b4::bf16lo(q.y), v[k + 3] = b4::bf16hi(q.y);
+      for (int k = 0; k < V / 4; ++k) {
+        const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i + 4 * k);
+        v[2 * k] = pair(b4::bf16lo(q.x), b4::bf16hi(q.x)), v[2 * k + 1] = pair(b4::bf16lo(q.y), b4::bf16hi(q.y));
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < V; k += 4) {
-        const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + k);
-        v[k] = q.x, v[k + 1] = q.y, v[k + 2] = q.z, v[k + 3] = q.w;
+      for (int k = 0; k < V / 4; ++k) {
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(static_cast<const float*>(p) + i + 4 * k);
+        v[2 * k] = q.x, v[2 * k + 1] = q.y;
       }
     }
   }
@@ -344,13 +388,13 @@ __device__ __forceinline__ void sum_shares(const char* first, const Params& p, i
   if (threadIdx.x >= p.G) return;
   const int lane = threadIdx.x & 31;
   for (int c = threadIdx.x * V; c < p.C; c += p.G * V, first += item) {
-    float d[V];
+    P2 d[V / 2];
     kept<V>(first, lane, d);
     for (int g = 1; g < NG; ++g) {
-      float more[V];
+      P2 more[V / 2];
       kept<V>(first + g * p.group_bytes, lane, more);
 #pragma unroll
-      for (int j = 0; j < V; ++j) d[j] += more[j];
+      for (int j = 0; j < V / 2; ++j) d[j] = add2(d[j], more[j]);
     }
     keep<V, 16>(reinterpret_cast<char*>(row + c), 0, d);
   }
@@ -359,14 +403,15 @@ __device__ __forceinline__ void sum_shares(const char* first, const Params& p, i
 // ---------------------------------------------------------------------------
 // A token's coefficients, fetched one token ahead: lane l of every warp loads
 // value l (and l + 32, ...), and the warp spreads them through a few floats
-// of shared memory of its own.  Order: P [SP, SP], then b [SP], then a [SP];
-// streams that are not there have zeros, absent arrays ones.
+// of shared memory of its own, each twice, to be read as pairs.  Order: P
+// [SP, SP] (TP: transposed), then b [SP], then a [SP]; streams that are not
+// there have zeros, absent arrays ones.
 // ---------------------------------------------------------------------------
-template <int SP, bool P, bool B, bool A>
+template <int SP, bool P, bool B, bool A, bool TP = false>
 struct Coefficients {
   static constexpr int NP = P ? SP * SP : 0, NB = NP + (B ? SP : 0), N = NB + (A ? SP : 0);
   static constexpr int CH = (N + 31) / 32;
-  static constexpr int FLOATS = (N + 3) / 4 * 4;
+  static constexpr int FLOATS = (2 * N + 3) / 4 * 4;
   // what this lane fetches is the same for every token: an address (or none,
   // and then a constant), a stride in bytes, a type
   const char* src[CH];
@@ -381,7 +426,7 @@ struct Coefficients {
       const Any* from = nullptr;
       int at = 0;
       if (n < NP) {
-        const int i = n / SP, j = n % SP;
+        const int i = TP ? n % SP : n / SP, j = TP ? n / SP : n % SP;
         if (i < p.S && j < p.S) from = p.P.p ? &p.P : nullptr, at = i * p.S + j, stride[c] = p.P_ts;
       } else if (n < NB) {
         if (n - NP < p.S) from = &p.b, at = n - NP, stride[c] = p.b_ts;
@@ -409,19 +454,19 @@ struct Coefficients {
     __syncwarp();  // the last token's readers are done
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      if (c * 32 + lane < FLOATS) s[c * 32 + lane] = next[c];
+      if (c * 32 + lane < N) reinterpret_cast<P2*>(s)[c * 32 + lane] = twice(next[c]);
     __syncwarp();
   }
-  __device__ __forceinline__ static void read(const float* s, int from, float (&v)[SP]) {
-    if constexpr (SP >= 4) {
+  // SP of them, from place `from` on.
+  __device__ __forceinline__ static void read(const float* s, int from, P2 (&v)[SP]) {
+    if constexpr (SP >= 2) {
 #pragma unroll
-      for (int i = 0; i < SP; i += 4) {
-        const float4 q = *reinterpret_cast<const float4*>(s + from + i);
-        v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
+      for (int i = 0; i < SP; i += 2) {
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(s + 2 * (from + i));
+        v[i] = q.x, v[i + 1] = q.y;
       }
     } else {
-#pragma unroll
-      for (int i = 0; i < SP; ++i) v[i] = s[from + i];
+      v[0] = *reinterpret_cast<const P2*>(s + 2 * from);
     }
   }
 };
@@ -531,10 +576,6 @@ __device__ __forceinline__ float of_total(const float (&total)[CH], int i) {
 // to fp32 on both sides and never overflows.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void gate_of(int act, float g, float& value, float& slope) {
-  if (act == HCB_ACT_LINEAR) {
-    value = g, slope = 1.0f;
-    return;
-  }
   const float e = __expf(-fabsf(g));
   const float inv = __fdividef(1.0f, 1.0f + e);
   const float s = g >= 0.0f ? inv : e * inv;
@@ -544,6 +585,26 @@ __device__ __forceinline__ void gate_of(int act, float g, float& value, float& s
     value = s, slope = s * rest;
   else
     value = g * s, slope = s * (1.0f + g * rest);
+}
+// The values of V gates replace them; their slopes, if wanted.
+template <int V, bool SLOPE>
+__device__ __forceinline__ void gates(int act, P2 (&g)[V / 2], P2 (&slope)[V / 2]) {
+  if (act == HCB_ACT_LINEAR) {
+    if constexpr (SLOPE) {
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) slope[j] = twice(1.0f);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < V / 2; ++j) {
+    float lo, hi, slo, shi;
+    split(g[j], lo, hi);
+    gate_of(act, lo, lo, slo);
+    gate_of(act, hi, hi, shi);
+    g[j] = pair(lo, hi);
+    if constexpr (SLOPE) slope[j] = pair(slo, shi);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -611,11 +672,11 @@ struct Need {
   size_t bytes(int C, int V, int G) const { return (size_t(G / 32) * of_warp(C, V, G) + group + 15) / 16 * 16; }
 };
 
-// Persistent launch of KERN, at most max_grid CTAs (the grid goes to *grid).
-// need(G, direct) is a Need; a shape that does not fit is shrunk, and made
-// direct (Params) where no group of 128 threads would do otherwise.
-template <auto KERN, class N>
-cudaError_t launch(Params p, Shape sh, int V, N&& need, int max_grid, int* grid, cudaStream_t s) {
+// The shape of a pass: need(G, direct) is a Need; a shape that does not fit is
+// shrunk, and made direct (Params) where no group of 128 threads would do
+// otherwise.  Fills in what a kernel has to know of it.
+template <class N>
+Shape plan(Params& p, Shape sh, int V, N&& need) {
   auto bytes = [&] { return need(sh.G, p.direct).bytes(p.C, V, sh.G); };
   p.direct = 0;
   while (bytes() * sh.NG > kSmemMax && sh.NG > 1) sh.NG /= 2;
@@ -624,9 +685,14 @@ cudaError_t launch(Params p, Shape sh, int V, N&& need, int max_grid, int* grid,
     p.direct = 1;
     while (bytes() > kSmemMax && sh.G > 32) sh.G = (sh.G / 2 + 31) / 32 * 32;
   }
-  const Need n = need(sh.G, p.direct);
   p.G = sh.G, p.group_bytes = static_cast<int32_t>(bytes());
-  p.warp_bytes = n.of_warp(p.C, V, sh.G);
+  p.warp_bytes = need(sh.G, p.direct).of_warp(p.C, V, sh.G);
+  return sh;
+}
+
+// Persistent launch of KERN, at most max_grid CTAs (the grid goes to *grid).
+template <auto KERN>
+cudaError_t launch(const Params& p, Shape sh, int max_grid, int* grid, cudaStream_t s) {
   const size_t smem = size_t(p.group_bytes) * sh.NG;
   int occ = 0;
   const cudaError_t e = resident<KERN>(sh.G * sh.NG, smem, &occ);
@@ -639,7 +705,10 @@ cudaError_t launch(Params p, Shape sh, int V, N&& need, int max_grid, int* grid,
 
 // Call F.operator()<SP, EXACT, TX, TY, V, ODD>() for the streams (SP of them:
 // 1, 2, 4 or 8; fewer, !EXACT, are rounded up, and the missing ones count as
-// zeros), the row types and alignment.  V elements are 16 bytes of the wider
+// zeros), the row types and alignment.  An EXACT kernel takes it further that
+// a mixing matrix comes with more than one stream and only with them, and
+// that the pass is not direct; a launcher takes the other kernel where that
+// does not hold.  V elements are 16 bytes of the wider
 // row type (8 bytes of bf16 at 8 streams, for the registers).
 template <int SP, bool EXACT, class F>
 cudaError_t by_type(int x_bf16, int y_bf16, bool vec, F&& f) {
@@ -674,5 +743,6 @@ cudaError_t enter_forward(const Params& p, int x_bf16, int y_bf16, bool vec, cud
 cudaError_t enter_backward(const Params& p, int x_bf16, int y_bf16, bool vec, int* rows, cudaStream_t s);
 cudaError_t leave_forward(const Params& p, int x_bf16, int y_bf16, bool vec, cudaStream_t s);
 cudaError_t leave_backward(const Params& p, int x_bf16, int y_bf16, bool vec, int* rows, cudaStream_t s);
+cudaError_t leave_enter_backward(const Params& p, int x_bf16, int y_bf16, bool vec, int* rows, cudaStream_t s);
 
 }  // namespace hcb

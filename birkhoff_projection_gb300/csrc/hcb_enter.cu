@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
   using RX = typename E::RX;
   using RY = typename E::RY;
   using Co = typename E::Co;
-  constexpr int DEPTH = E::DEPTH;
+  constexpr int DEPTH = E::DEPTH, H = V / 2;
   extern __shared__ __align__(16) char smem[];
   const int G = p.G, NG = blockDim.x / G, group = threadIdx.x / G, l = threadIdx.x % G;
   const int lane = threadIdx.x & 31, warp = l / 32, C = p.C, S = EXACT ? SP : p.S, GV = G * V;
@@ -79,47 +79,49 @@ __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
   for (int d = 0; d < DEPTH; ++d) copy_next();
 
   const char* slot = ring;
+#pragma unroll 1
   for (; t < p.T; t += step) {
     co.spread(co_s, lane);
     if (t + step < p.T) co.fetch(t + step);
-    float a[SP];
+    P2 a[SP];
     Co::read(co_s, Co::NB, a);
     const TX* x = at_row<TX>(p.x, t, p.x_ts);
-    float ss[1] = {0.0f};
+    P2 ss = 0;
     char* item = item0;
+#pragma unroll 1
     for (int c = l * V, k = 0; k < K; ++k, c += GV, item += E::ITEM) {
       copy_wait<DEPTH - 1>();
-      float u[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) u[j] = 0.0f;
+      P2 u[H] = {};
       if (c < C) {
 #pragma unroll
         for (int i = 0; i < SP; ++i) {
           if (EXACT || i < S) {
-            float xv[V];
+            P2 xv[H];
             RX::arrived(slot + i * RX::SLOT, lane, x + i * p.x_ss + c, xv);
 #pragma unroll
-            for (int j = 0; j < V; ++j) u[j] += a[i] * xv[j];
+            for (int j = 0; j < H; ++j) u[j] = fma2(a[i], xv[j], u[j]);
           }
         }
       }
       copy_next();
       slot = slot == ring + (DEPTH - 1) * E::SLOT ? ring : slot + E::SLOT;
 #pragma unroll
-      for (int j = 0; j < V; ++j) ss[0] += u[j] * u[j];
+      for (int j = 0; j < H; ++j) ss = fma2(u[j], u[j], ss);
       keep<V>(item, lane, u);
     }
+    const float sum[1] = {both(ss)};
     float total[1];
-    GroupSum<1>::run(ss, total, red, turn, G, group, lane, warp);
-    const float r = rsqrtf(of_total(total, 0) * inv_c + p.eps);
+    GroupSum<1>::run(sum, total, red, turn, G, group, lane, warp);
+    const P2 r = twice(rsqrtf(of_total(total, 0) * inv_c + p.eps));
     TY* h = static_cast<TY*>(p.h) + uint64_t(t) * uint32_t(C);
     item = item0;
+#pragma unroll 1
     for (int c = l * V; c < C; c += GV, item += E::ITEM) {
-      float u[V], w[V];
+      P2 u[H], w[H];
       kept<V>(item, lane, u);
       p.w.load<V, ODD>(c, C - c, w);
 #pragma unroll
-      for (int j = 0; j < V; ++j) u[j] *= r * w[j];
+      for (int j = 0; j < H; ++j) u[j] = mul2(u[j], mul2(r, w[j]));
       RY::store(h + c, u, C - c);
     }
   }
@@ -153,12 +155,13 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
   using RY = typename E::RY;
   using Co = typename E::Co;
   using Sum = typename E::Sum;
-  constexpr int DEPTH = E::DEPTH;
+  constexpr int DEPTH = E::DEPTH, H = V / 2;
   extern __shared__ __align__(16) char smem[];
   const int G = p.G, NG = blockDim.x / G, group = threadIdx.x / G, l = threadIdx.x % G;
   const int lane = threadIdx.x & 31, warp = l / 32, C = p.C, S = EXACT ? SP : p.S, GV = G * V;
   const int K = (C + GV - 1) / GV;
-  const int ITEM = p.direct ? E::KW : E::ITEM;
+  const bool direct = !EXACT && p.direct;
+  const int ITEM = direct ? E::KW : E::ITEM;
   char* of_group = smem + group * p.group_bytes;
   char* ring = of_group + warp * p.warp_bytes;
   char* item0 = ring + DEPTH * E::SLOT;
@@ -167,7 +170,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
   float* red = co_all + G / 32 * Co::FLOATS;
   Sum::clear(red, G, l);
   group_sync(G, group);
-  float* row_dw = p.direct && p.dw ? p.dw + int64_t(blockIdx.x) * pitch(C) : nullptr;
+  float* row_dw = direct && p.dw ? p.dw + int64_t(blockIdx.x) * pitch(C) : nullptr;
   int turn = 0;
   const float inv_c = 1.0f / static_cast<float>(C);
   const uint32_t step = gridDim.x * NG;
@@ -203,8 +206,9 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) copy_next();
   if (p.dw) {
-    const float z[V] = {};
+    const P2 z[H] = {};
     char* item = item0;
+#pragma unroll 1
     for (int c = l * V; c < C; c += GV, item += ITEM) {
       if (row_dw)
         keep<V, 16>(reinterpret_cast<char*>(row_dw + c), 0, z);
@@ -214,43 +218,41 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
   }
 
   const char* slot = ring;
+#pragma unroll 1
   for (; t < p.T; t += step) {
     co.spread(co_s, lane);
     if (t + step < p.T) co.fetch(t + step);
-    float a[SP];
+    P2 a[SP];
     Co::read(co_s, Co::NB, a);
     const TX* x = at_row<TX>(p.x, t, p.x_ts);
     const TY* dh = at_row<TY>(p.dh, t, p.dh_ts);
-    float sum[2 * SP];
-#pragma unroll
-    for (int s = 0; s < 2 * SP; ++s) sum[s] = 0.0f;
+    P2 sum2[2 * SP] = {};
     char* item = item0;
+#pragma unroll 1
     for (int c = l * V, k = 0; k < K; ++k, c += GV, item += ITEM) {
-      float w[V];
-      if (c < C) p.w.load<V, ODD>(c, C - c, w);
       copy_wait<DEPTH - 1>();
       if (c < C) {
-        float xv[SP][V], g[V], u[V];
+        P2 xv[SP][H], g[H], w[H], u[H] = {};
+        p.w.load<V, ODD>(c, C - c, w);
 #pragma unroll
         for (int i = 0; i < SP; ++i) {
           if (EXACT || i < S) {
             RX::arrived(slot + i * RX::SLOT, lane, x + i * p.x_ss + c, xv[i]);
-          } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) xv[i][j] = 0.0f;
+            for (int j = 0; j < H; ++j) u[j] = fma2(a[i], xv[i][j], u[j]);
           }
         }
         RY::arrived_kept(slot + E::DH, lane, dh + c, g, item + E::KH);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          g[j] *= w[j];
-          u[j] = 0.0f;
+        for (int j = 0; j < H; ++j) g[j] = mul2(g[j], w[j]);
 #pragma unroll
-          for (int s = 0; s < SP; ++s) u[j] += a[s] * xv[s][j];
+        for (int i = 0; i < SP; ++i) {
+          if (EXACT || i < S) {
 #pragma unroll
-          for (int s = 0; s < SP; ++s) {
-            sum[s] += g[j] * xv[s][j];
-            sum[SP + s] += u[j] * xv[s][j];
+            for (int j = 0; j < H; ++j) {
+              sum2[i] = fma2(g[j], xv[i][j], sum2[i]);
+              sum2[SP + i] = fma2(u[j], xv[i][j], sum2[SP + i]);
+            }
           }
         }
         keep<V>(item, lane, u);
@@ -258,13 +260,15 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
       copy_next();
       slot = slot == ring + (DEPTH - 1) * E::SLOT ? ring : slot + E::SLOT;
     }
-    float total[1];
+    float sum[2 * SP], total[1];
+#pragma unroll
+    for (int i = 0; i < 2 * SP; ++i) sum[i] = both(sum2[i]);
     Sum::run(sum, total, red, turn, G, group, lane, warp);
     float gu = 0.0f, uu = 0.0f;
 #pragma unroll
     for (int s = 0; s < SP; ++s) {
-      gu += a[s] * of_total(total, s);
-      uu += a[s] * of_total(total, SP + s);
+      gu += low(a[s]) * of_total(total, s);
+      uu += low(a[s]) * of_total(total, SP + s);
     }
     const float r = rsqrtf(uu * inv_c + p.eps);
     const float k_u = gu * inv_c * r * r;
@@ -272,37 +276,32 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
       const float u_x = __shfl_sync(0xffffffffu, total[0], (lane + SP) & 31);
       if (warp == 0 && lane < S) put_any(p.da, p.a.bf16, int64_t(t) * S + lane, r * (total[0] - k_u * u_x));
     }
+    // r u is what the weight's share takes, and du = r w dh - k (r u)
+    const P2 r2 = twice(r), minus_k = twice(-k_u);
     const TX* dres = p.dres ? at_row<TX>(p.dres, t, p.dres_ts) : nullptr;
     TX* dx = p.dx ? static_cast<TX*>(p.dx) + uint64_t(t) * uint32_t(S * C) : nullptr;
     item = item0;
+#pragma unroll 1
     for (int c = l * V, k = 0; k < K; ++k, c += GV, item += ITEM) {
       if (dres) copy_wait<DEPTH - 1>();
       if (c < C) {
-        float u[V], g[V], w[V];
+        P2 u[H], g[H], w[H];
         kept<V>(item, lane, u);
         RY::kept(item + E::KH, lane, g);
         p.w.load<V, ODD>(c, C - c, w);
-        if (p.dw) {
-          float d[V];
 #pragma unroll
-          for (int j = 0; j < V; ++j) d[j] = g[j] * (u[j] * r);
-          add_share<V>(item + E::KW, lane, row_dw ? row_dw + c : nullptr, d);
-        }
+        for (int j = 0; j < H; ++j) u[j] = mul2(r2, u[j]);
+        if (p.dw) add_share<V>(item + E::KW, lane, row_dw ? row_dw + c : nullptr, g, u);
 #pragma unroll
-        for (int j = 0; j < V; ++j) u[j] = r * (g[j] * w[j] - k_u * u[j]);
+        for (int j = 0; j < H; ++j) u[j] = fma2(mul2(r2, w[j]), g[j], mul2(minus_k, u[j]));
         if (dx) {
 #pragma unroll
           for (int i = 0; i < SP; ++i) {
             if (EXACT || i < S) {
-              float d[V];
-              if (dres) {
-                RX::arrived(slot + i * RX::SLOT, lane, dres + i * p.dres_ss + c, d);
+              P2 d[H] = {};
+              if (dres) RX::arrived(slot + i * RX::SLOT, lane, dres + i * p.dres_ss + c, d);
 #pragma unroll
-                for (int j = 0; j < V; ++j) d[j] += a[i] * u[j];
-              } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j) d[j] = a[i] * u[j];
-              }
+              for (int j = 0; j < H; ++j) d[j] = fma2(a[i], u[j], d[j]);
               RX::store(dx + i * C + c, d, C - c);
             }
           }
@@ -315,7 +314,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
     }
   }
   copy_wait_all();
-  if (p.dw && !p.direct) {
+  if (p.dw && !direct) {
     __syncthreads();
     sum_shares<V>(smem + warp * p.warp_bytes + DEPTH * E::SLOT + E::KW, p, NG, ITEM,
                   p.dw + int64_t(blockIdx.x) * pitch(C));
@@ -329,9 +328,10 @@ struct Forward {
   cudaStream_t s;
   template <int SP, bool EXACT, class TX, class TY, int V, bool ODD>
   cudaError_t operator()() const {
+    Params q = p;
     int grid;
-    return launch<enter_kernel<SP, EXACT, TX, TY, V, ODD>>(
-        p, shape_of(p.T, p.C, V, HCB_ENTER_PER, kMaxGroup), V, Enter<SP, TX, TY, V, ODD>::need, 1 << 30, &grid, s);
+    const Shape sh = plan(q, shape_of(p.T, p.C, V, HCB_ENTER_PER, kMaxGroup), V, Enter<SP, TX, TY, V, ODD>::need);
+    return launch<enter_kernel<SP, EXACT, TX, TY, V, ODD>>(q, sh, 1 << 30, &grid, s);
   }
 };
 struct Backward {
@@ -340,9 +340,12 @@ struct Backward {
   cudaStream_t s;
   template <int SP, bool EXACT, class TX, class TY, int V, bool ODD>
   cudaError_t operator()() const {
-    return launch<enter_backward_kernel<SP, EXACT, TX, TY, V, ODD>>(
-        p, shape_of(p.T, p.C, V, HCB_ENTER_BWD_PER, kMaxGroup), V, EnterBackward<SP, TX, TY, V, ODD>::need,
-        p.dw ? kMaxRows : 1 << 30, rows, s);
+    Params q = p;
+    const Shape sh =
+        plan(q, shape_of(p.T, p.C, V, HCB_ENTER_BWD_PER, kMaxGroup), V, EnterBackward<SP, TX, TY, V, ODD>::need);
+    const int most = p.dw ? kMaxRows : 1 << 30;
+    if (EXACT && !q.direct) return launch<enter_backward_kernel<SP, EXACT, TX, TY, V, ODD>>(q, sh, most, rows, s);
+    return launch<enter_backward_kernel<SP, false, TX, TY, V, ODD>>(q, sh, most, rows, s);
   }
 };
 

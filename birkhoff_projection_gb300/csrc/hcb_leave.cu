@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
   using RX = typename E::RX;
   using RY = typename E::RY;
   using Co = typename E::Co;
-  constexpr int DEPTH = E::DEPTH;
+  constexpr int DEPTH = E::DEPTH, H = V / 2;
   extern __shared__ __align__(16) char smem[];
   const int G = p.G, NG = blockDim.x / G, group = threadIdx.x / G, l = threadIdx.x % G;
   const int lane = threadIdx.x & 31, warp = l / 32, C = p.C, S = EXACT ? SP : p.S, GV = G * V;
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
   group_sync(G, group);
   int turn = 0, turn_next = 0;
   const float inv_c = 1.0f / static_cast<float>(C);
-  const bool mix = p.P.p != nullptr, gated = p.gate != nullptr;
+  const bool mix = EXACT ? SP > 1 : p.P.p != nullptr, gated = p.gate != nullptr;
   const uint32_t step = gridDim.x * NG;
   uint32_t t = blockIdx.x * NG + group;
 
@@ -88,35 +88,33 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
   for (int d = 0; d < DEPTH; ++d) copy_next();
 
   const char* slot = ring;
+#pragma unroll 1
   for (; t < p.T; t += step) {
     co.spread(co_s, lane);
     if (t + step < p.T) co.fetch(t + step);
     const TX* x = at_row<TX>(p.x, t, p.x_ts);
     const TY* y = at_row<TY>(p.y, t, p.y_ts);
     const TY* gate = at_row<TY>(p.gate, t, p.gate_ts);
-    float ss[1] = {0.0f};
+    P2 ss = 0;
     char* item = item0;
+#pragma unroll 1
     for (int c = l * V, k = 0; k < K; ++k, c += GV, item += E::ITEM) {
-      float w[V];
-      if (c < C) p.w.load<V, ODD>(c, C - c, w);
       copy_wait<DEPTH - 1>();
       if (c < C) {
-        float v[V];
+        P2 v[H], w[H];
+        p.w.load<V, ODD>(c, C - c, w);
         RY::arrived(slot + E::Y, lane, y + c, v);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          ss[0] += v[j] * v[j];
-          v[j] *= w[j];
+        for (int j = 0; j < H; ++j) {
+          ss = fma2(v[j], v[j], ss);
+          v[j] = mul2(v[j], w[j]);
         }
         if (gated) {
-          float g[V];
+          P2 g[H];
           RY::arrived(slot + E::Y + RY::SLOT, lane, gate + c, g);
+          gates<V, false>(p.act, g, w);
 #pragma unroll
-          for (int j = 0; j < V; ++j) {
-            float q, slope;
-            gate_of(p.act, g[j], q, slope);
-            v[j] *= q;
-          }
+          for (int j = 0; j < H; ++j) v[j] = mul2(v[j], g[j]);
         }
         keep<V>(item, lane, v);
       }
@@ -125,25 +123,23 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
     }
     float rho = p.scale;
     if (p.norm) {
+      const float sum[1] = {both(ss)};
       float total[1];
-      GroupSum<1>::run(ss, total, red, turn, G, group, lane, warp);
+      GroupSum<1>::run(sum, total, red, turn, G, group, lane, warp);
       rho *= rsqrtf(of_total(total, 0) * inv_c + p.eps);
     }
-    float P[SP][SP], b[SP], a[SP];
+    P2 b[SP];
     Co::read(co_s, Co::NP, b);
-    Co::read(co_s, Co::NB, a);
 #pragma unroll
-    for (int i = 0; i < SP; ++i) {
-      Co::read(co_s, i * SP, P[i]);
-      b[i] *= rho;
-    }
+    for (int i = 0; i < SP; ++i) b[i] = mul2(b[i], twice(rho));
     TX* out = static_cast<TX*>(p.out) + uint64_t(t) * uint32_t(S * C);
-    ss[0] = 0.0f;
+    ss = 0;
     item = item0;
+#pragma unroll 1
     for (int c = l * V, k = 0; k < K; ++k, c += GV, item += E::ITEM) {
       copy_wait<DEPTH - 1>();
       if (c < C) {
-        float v[V], xv[SP][V], u[V];
+        P2 v[H], xv[SP][H], u[H] = {};
         kept<V>(item, lane, v);
 #pragma unroll
         for (int i = 0; i < SP; ++i) {
@@ -151,36 +147,40 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
             RX::arrived(slot + i * RX::SLOT, lane, x + i * p.x_ss + c, xv[i]);
           } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) xv[i][j] = 0.0f;
+            for (int j = 0; j < H; ++j) xv[i][j] = 0;
           }
         }
-#pragma unroll
-        for (int j = 0; j < V; ++j) u[j] = 0.0f;
+        P2 a[SP];
+        if (p.h) Co::read(co_s, Co::NB, a);
 #pragma unroll
         for (int i = 0; i < SP; ++i) {
           if (EXACT || i < S) {
-            float o[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) o[j] = b[i] * v[j];
+            P2 o[H];
             if (mix) {
+              P2 P[SP];
+              Co::read(co_s, i * SP, P);
 #pragma unroll
-              for (int q = 0; q < SP; ++q)
+              for (int j = 0; j < H; ++j) {
+                o[j] = mul2(b[i], v[j]);
 #pragma unroll
-                for (int j = 0; j < V; ++j) o[j] += P[i][q] * xv[q][j];
+                for (int q = 0; q < SP; ++q) o[j] = fma2(P[q], xv[q][j], o[j]);
+              }
             } else {
 #pragma unroll
-              for (int j = 0; j < V; ++j) o[j] += xv[i][j];
+              for (int j = 0; j < H; ++j) o[j] = fma2(b[i], v[j], xv[i][j]);
             }
-            RX::store(out + i * C + c, o, C - c);
             if (p.h) {
+              RX::store_rounded(out + i * C + c, o, C - c);
 #pragma unroll
-              for (int j = 0; j < V; ++j) u[j] += a[i] * RX::round(o[j]);
+              for (int j = 0; j < H; ++j) u[j] = fma2(a[i], o[j], u[j]);
+            } else {
+              RX::store(out + i * C + c, o, C - c);
             }
           }
         }
         if (p.h) {
 #pragma unroll
-          for (int j = 0; j < V; ++j) ss[0] += u[j] * u[j];  // past C: y, x and so u are zeros
+          for (int j = 0; j < H; ++j) ss = fma2(u[j], u[j], ss);  // past C: y, x and so u are zeros
           keep<V>(item, lane, u);
         }
       }
@@ -188,17 +188,19 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
       slot = slot == ring + (DEPTH - 1) * E::SLOT ? ring : slot + E::SLOT;
     }
     if (p.h) {
+      const float sum[1] = {both(ss)};
       float total[1];
-      GroupSum<1>::run(ss, total, red_next, turn_next, G, group, lane, warp);
-      const float r = rsqrtf(of_total(total, 0) * inv_c + p.eps_next);
+      GroupSum<1>::run(sum, total, red_next, turn_next, G, group, lane, warp);
+      const P2 r = twice(rsqrtf(of_total(total, 0) * inv_c + p.eps_next));
       TY* h = static_cast<TY*>(p.h) + uint64_t(t) * uint32_t(C);
       item = item0;
+#pragma unroll 1
       for (int c = l * V; c < C; c += GV, item += E::ITEM) {
-        float u[V], w[V];
+        P2 u[H], w[H];
         kept<V>(item, lane, u);
         p.wn.load<V, ODD>(c, C - c, w);
 #pragma unroll
-        for (int j = 0; j < V; ++j) u[j] *= r * w[j];
+        for (int j = 0; j < H; ++j) u[j] = mul2(u[j], mul2(r, w[j]));
         RY::store(h + c, u, C - c);
       }
     }
@@ -213,10 +215,13 @@ struct Forward {
   cudaStream_t s;
   template <int SP, bool EXACT, class TX, class TY, int V, bool ODD>
   cudaError_t operator()() const {
+    Params q = p;
     int grid;
-    return launch<leave_kernel<SP, EXACT, TX, TY, V, ODD>>(
-        p, shape_of(p.T, p.C, V, HCB_LEAVE_PER, SP == 8 ? 256 : kMaxGroup), V, Leave<SP, TX, TY, V, ODD>::need,
-        1 << 30, &grid, s);
+    const Shape sh =
+        plan(q, shape_of(p.T, p.C, V, HCB_LEAVE_PER, SP == 8 ? 256 : kMaxGroup), V, Leave<SP, TX, TY, V, ODD>::need);
+    if (EXACT && (p.P.p != nullptr) == (SP > 1))
+      return launch<leave_kernel<SP, EXACT, TX, TY, V, ODD>>(q, sh, 1 << 30, &grid, s);
+    return launch<leave_kernel<SP, false, TX, TY, V, ODD>>(q, sh, 1 << 30, &grid, s);
   }
 };
 

@@ -1,0 +1,416 @@
+// hcb_leave_bwd.cuh -- the gradient of leave and of leave_enter
+// (hcb_leave_backward of include/hc_block.h); instantiated in hcb_leave_bwd.cu
+// and hcb_leave_enter_bwd.cu.
+#pragma once
+
+#include "hcb_common.cuh"
+
+#ifndef HCB_LEAVE_BWD_DEPTH
+#define HCB_LEAVE_BWD_DEPTH 1
+#endif
+#ifndef HCB_LEAVE_BWD_MINB1
+#define HCB_LEAVE_BWD_MINB1 3
+#endif
+#ifndef HCB_LEAVE_BWD_MINB2
+#define HCB_LEAVE_BWD_MINB2 2
+#endif
+#ifndef HCB_LEAVE_BWD_PER
+#define HCB_LEAVE_BWD_PER 2
+#endif
+
+namespace hcb {
+
+// Every sum that the gradient needs is linear in what is read, up to the
+// factor rho of y's norm: with q = act(gate) and e = w q y,
+//   dP_ij = <D_i, x_j>,  db_i = scale rho <D_i, e>,
+//   <g, y> = scale sum_i b_i <D_i, e>
+// so one pass over the row finds S^2 + S + 1 sums and writes dx.  It keeps
+// q dv and act'(gate) w y dv (dv = sum_i b_i D_i), of which a second one
+// writes dy, dgate and the weight's shares.
+// NEXT adds a run of items before it: D_i = dout_i + a_i du with du from dh,
+// as in enter_backward_kernel.
+template <int SP, class TX, class TY, int V, bool ODD, bool NEXT>
+struct LeaveBackward {
+  using RX = Row<TX, V, ODD>;
+  using RY = Row<TY, V, ODD>;
+  using Co = Coefficients<SP, true, true, NEXT, true>;
+  // the sums: dP (by column), <D_i, e>, <y, y>
+  static constexpr int R = SP * SP + SP + 1;
+  using Sum = GroupSum<R>;
+  using SumNext = GroupSum<2 * SP>;
+  static constexpr int DEPTH = HCB_LEAVE_BWD_DEPTH;
+  static constexpr int MINB = SP == 1 ? HCB_LEAVE_BWD_MINB1 : SP == 2 ? HCB_LEAVE_BWD_MINB2 : SP == 4 ? 2 : 1;
+  // a slot: dout, y, gate and x; or the stored result, and dh where y would be
+  static constexpr int Y = SP * RX::SLOT, GATE = Y + RY::SLOT, X = GATE + RY::SLOT;
+  __host__ __device__ static constexpr int slot(bool mix, bool gated) {
+    return mix ? X + SP * RX::SLOT : gated ? X : GATE;
+  }
+  // kept: q dv (before it, NEXT: the next block's u); y; NEXT: dh; the shares
+  // of dw and of dw_next; act' w y dv.  direct: the first and the last only.
+  static constexpr int F = kFloats<V>, KY = F, KH = KY + RY::KEPT, KW = KH + (NEXT ? RY::KEPT : 0), KN = KW + F,
+                       KB = KN + (NEXT ? F : 0);
+  __host__ __device__ static constexpr int kb(int direct) { return direct ? F : KB; }
+  __host__ __device__ static constexpr int item(bool gated, int direct) { return kb(direct) + (gated ? F : 0); }
+};
+
+// GATE: 0 no gate, 1 a gate, 2 told at run time.
+template <int SP, bool EXACT, class TX, class TY, int V, bool ODD, bool NEXT, int GATE>
+__global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::MINB) leave_backward_kernel(const Params p) {
+  using E = LeaveBackward<SP, TX, TY, V, ODD, NEXT>;
+  using RX = typename E::RX;
+  using RY = typename E::RY;
+  using Co = typename E::Co;
+  using Sum = typename E::Sum;
+  constexpr int R = E::R, DEPTH = E::DEPTH, H = V / 2;
+  extern __shared__ __align__(16) char smem[];
+  const int G = p.G, NG = blockDim.x / G, group = threadIdx.x / G, l = threadIdx.x % G;
+  const int lane = threadIdx.x & 31, warp = l / 32, C = p.C, S = EXACT ? SP : p.S, GV = G * V;
+  const int K = (C + GV - 1) / GV;
+  const bool direct = !EXACT && p.direct;
+  const bool mix = EXACT ? SP > 1 : p.P.p != nullptr, gated = GATE == 2 ? p.gate != nullptr : GATE != 0;
+  const int SLOT = E::slot(mix, gated), ITEM = E::item(gated, direct), KB = E::kb(direct);
+  char* of_group = smem + group * p.group_bytes;
+  char* ring = of_group + warp * p.warp_bytes;
+  char* item0 = ring + DEPTH * SLOT;
+  float* co_all = reinterpret_cast<float*>(of_group + G / 32 * p.warp_bytes);
+  float* co_s = co_all + warp * Co::FLOATS;
+  float* red = co_all + G / 32 * Co::FLOATS;
+  float* red_next = red + Sum::floats(G);
+  Sum::clear(red, G, l);
+  if constexpr (NEXT) E::SumNext::clear(red_next, G, l);
+  group_sync(G, group);
+  float* row_dw = direct && p.dw ? p.dw + int64_t(blockIdx.x) * pitch(C) : nullptr;
+  float* row_dwn = NEXT && direct && p.dwn ? p.dwn + int64_t(blockIdx.x) * pitch(C) : nullptr;
+  int turn = 0, turn_next = 0;
+  const float inv_c = 1.0f / static_cast<float>(C);
+  const uint32_t step = gridDim.x * NG;
+  uint32_t t = blockIdx.x * NG + group;
+
+  const int NI = NEXT ? 2 * K : K;
+  uint32_t ta = t;
+  int ca = l * V, ia = 0;
+  char* slot_a = ring;
+  auto copy_next = [&] {
+    if (ta < p.T && ca < C) {
+      if (NEXT && ia < K) {
+        const TX* o = at_row<TX>(p.out_in, ta, p.out_ts) + ca;
+#pragma unroll
+        for (int i = 0; i < SP; ++i)
+          if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, o + i * p.out_ss, C - ca);
+        RY::copy(slot_a + E::Y, lane, at_row<TY>(p.dh, ta, p.dh_ts) + ca, C - ca);
+      } else {
+        const TX* d = at_row<TX>(p.dout, ta, p.dout_ts) + ca;
+#pragma unroll
+        for (int i = 0; i < SP; ++i)
+          if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, d + i * p.dout_ss, C - ca);
+        RY::copy(slot_a + E::Y, lane, at_row<TY>(p.y, ta, p.y_ts) + ca, C - ca);
+        if (gated) RY::copy(slot_a + E::GATE, lane, at_row<TY>(p.gate, ta, p.gate_ts) + ca, C - ca);
+        if (mix) {
+          const TX* x = at_row<TX>(p.x, ta, p.x_ts) + ca;
+#pragma unroll
+          for (int i = 0; i < SP; ++i)
+            if (EXACT || i < S) RX::copy(slot_a + E::X + i * RX::SLOT, lane, x + i * p.x_ss, C - ca);
+        }
+      }
+    }
+    copy_commit();
+    ca += GV;
+    ++ia;
+    if (NEXT && ia == K) ca = l * V;
+    if (ia == NI) ia = 0, ca = l * V, ta += step;
+    if constexpr (DEPTH > 1) slot_a = slot_a == ring + (DEPTH - 1) * SLOT ? ring : slot_a + SLOT;
+  };
+  Co co;
+  co.init(p, lane);
+  if (t < p.T) co.fetch(t);
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) copy_next();
+  {
+    const P2 z[H] = {};
+    char* item = item0;
+#pragma unroll 1
+    for (int c = l * V; c < C; c += GV, item += ITEM) {
+      if (direct) {
+        if (row_dw) keep<V, 16>(reinterpret_cast<char*>(row_dw + c), 0, z);
+        if (NEXT && row_dwn) keep<V, 16>(reinterpret_cast<char*>(row_dwn + c), 0, z);
+      } else {
+        keep<V>(item + E::KW, lane, z);
+        if constexpr (NEXT) keep<V>(item + E::KN, lane, z);
+      }
+    }
+  }
+
+  const char* slot = ring;
+#pragma unroll 1
+  for (; t < p.T; t += step) {
+    co.spread(co_s, lane);
+    if (t + step < p.T) co.fetch(t + step);
+    float r_next = 0.0f, k_next = 0.0f;
+    if constexpr (NEXT) {
+      const TX* o = at_row<TX>(p.out_in, t, p.out_ts);
+      const TY* dh = at_row<TY>(p.dh, t, p.dh_ts);
+      P2 a[SP], sum2[2 * SP] = {};
+      Co::read(co_s, Co::NB, a);
+      char* item = item0;
+#pragma unroll 1
+      for (int c = l * V, k = 0; k < K; ++k, c += GV, item += ITEM) {
+        copy_wait<DEPTH - 1>();
+        if (c < C) {
+          P2 xv[SP][H], g[H], w[H], u[H] = {};
+          p.wn.load<V, ODD>(c, C - c, w);
+#pragma unroll
+          for (int i = 0; i < SP; ++i) {
+            if (EXACT || i < S) {
+              RX::arrived(slot + i * RX::SLOT, lane, o + i * p.out_ss + c, xv[i]);
+#pragma unroll
+              for (int j = 0; j < H; ++j) u[j] = fma2(a[i], xv[i][j], u[j]);
+            }
+          }
+          if (direct)
+            RY::arrived(slot + E::Y, lane, dh + c, g);
+          else
+            RY::arrived_kept(slot + E::Y, lane, dh + c, g, item + E::KH);
+#pragma unroll
+          for (int j = 0; j < H; ++j) g[j] = mul2(g[j], w[j]);
+#pragma unroll
+          for (int i = 0; i < SP; ++i) {
+            if (EXACT || i < S) {
+#pragma unroll
+              for (int j = 0; j < H; ++j) {
+                sum2[i] = fma2(g[j], xv[i][j], sum2[i]);
+                sum2[SP + i] = fma2(u[j], xv[i][j], sum2[SP + i]);
+              }
+            }
+          }
+          keep<V>(item, lane, u);
+        }
+        copy_next();
+        if constexpr (DEPTH > 1) slot = slot == ring + (DEPTH - 1) * SLOT ? ring : slot + SLOT;
+      }
+      float sum[2 * SP], total[1];
+#pragma unroll
+      for (int i = 0; i < 2 * SP; ++i) sum[i] = both(sum2[i]);
+      E::SumNext::run(sum, total, red_next, turn_next, G, group, lane, warp);
+      float gu = 0.0f, uu = 0.0f;
+#pragma unroll
+      for (int s = 0; s < SP; ++s) {
+        gu += low(a[s]) * of_total(total, s);
+        uu += low(a[s]) * of_total(total, SP + s);
+      }
+      r_next = rsqrtf(uu * inv_c + p.eps_next);
+      k_next = gu * inv_c * r_next * r_next;
+      if (p.da) {
+        const float u_x = __shfl_sync(0xffffffffu, total[0], (lane + SP) & 31);
+        if (warp == 0 && lane < S)
+          put_any(p.da, p.a.bf16, int64_t(t) * S + lane, r_next * (total[0] - k_next * u_x));
+      }
+    }
+    const TX* dout = at_row<TX>(p.dout, t, p.dout_ts);
+    const TX* x = at_row<TX>(p.x, t, p.x_ts);
+    const TY* y = at_row<TY>(p.y, t, p.y_ts);
+    const TY* gate = at_row<TY>(p.gate, t, p.gate_ts);
+    P2 sum2[R] = {};
+    TX* dx = p.dx ? static_cast<TX*>(p.dx) + uint64_t(t) * uint32_t(S * C) : nullptr;
+    char* item = item0;
+#pragma unroll 1
+    for (int c = l * V, k = 0; k < K; ++k, c += GV, item += ITEM) {
+      P2 du[H];
+      if (NEXT && c < C) {
+        P2 h[H], wn[H];
+        const P2 r2 = twice(r_next), minus_k = twice(-k_next);
+        kept<V>(item, lane, du);
+        if (direct)
+          RY::load(at_row<TY>(p.dh, t, p.dh_ts) + c, h, C - c);
+        else
+          RY::kept(item + E::KH, lane, h);
+        p.wn.load<V, ODD>(c, C - c, wn);
+#pragma unroll
+        for (int j = 0; j < H; ++j) du[j] = mul2(r2, du[j]);
+        if (p.dwn) add_share<V>(item + E::KN, lane, row_dwn ? row_dwn + c : nullptr, h, du);
+#pragma unroll
+        for (int j = 0; j < H; ++j) du[j] = fma2(mul2(r2, wn[j]), h[j], mul2(minus_k, du[j]));
+      }
+      copy_wait<DEPTH - 1>();
+      if (c >= C) {
+        copy_next();
+        if constexpr (DEPTH > 1) slot = slot == ring + (DEPTH - 1) * SLOT ? ring : slot + SLOT;
+        continue;
+      }
+      P2 D[SP][H], e[H], g[H];
+#pragma unroll
+      for (int i = 0; i < SP; ++i) {
+        if (EXACT || i < S) {
+          RX::arrived(slot + i * RX::SLOT, lane, dout + i * p.dout_ss + c, D[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < H; ++j) D[i][j] = 0;
+        }
+      }
+      if constexpr (NEXT) {
+        P2 a[SP];
+        Co::read(co_s, Co::NB, a);
+#pragma unroll
+        for (int i = 0; i < SP; ++i)
+#pragma unroll
+          for (int j = 0; j < H; ++j) D[i][j] = fma2(a[i], du[j], D[i][j]);
+      }
+      if (mix) {
+#pragma unroll
+        for (int q = 0; q < SP; ++q) {
+          if (EXACT || q < S) {
+            P2 xv[H];
+            RX::arrived(slot + E::X + q * RX::SLOT, lane, x + q * p.x_ss + c, xv);
+#pragma unroll
+            for (int i = 0; i < SP; ++i)
+#pragma unroll
+              for (int j = 0; j < H; ++j) sum2[q * SP + i] = fma2(D[i][j], xv[j], sum2[q * SP + i]);
+          }
+        }
+      }
+      if (direct)
+        RY::arrived(slot + E::Y, lane, y + c, e);
+      else
+        RY::arrived_kept(slot + E::Y, lane, y + c, e, item + E::KY);
+      if (gated) RY::arrived(slot + E::GATE, lane, gate + c, g);
+      copy_next();
+      if constexpr (DEPTH > 1) slot = slot == ring + (DEPTH - 1) * SLOT ? ring : slot + SLOT;
+      if (dx) {
+#pragma unroll
+        for (int q = 0; q < SP; ++q) {
+          if (EXACT || q < S) {
+            if (mix) {
+              P2 d[H], P[SP];
+              Co::read(co_s, q * SP, P);
+#pragma unroll
+              for (int j = 0; j < H; ++j) {
+                d[j] = mul2(P[0], D[0][j]);
+#pragma unroll
+                for (int i = 1; i < SP; ++i) d[j] = fma2(P[i], D[i][j], d[j]);
+              }
+              RX::store(dx + q * C + c, d, C - c);
+            } else {
+              RX::store(dx + q * C + c, D[q], C - c);
+            }
+          }
+        }
+      }
+      P2 dv[H], b[SP];
+      Co::read(co_s, Co::NP, b);
+#pragma unroll
+      for (int j = 0; j < H; ++j) {
+        dv[j] = mul2(b[0], D[0][j]);
+#pragma unroll
+        for (int i = 1; i < SP; ++i) dv[j] = fma2(b[i], D[i][j], dv[j]);
+        sum2[SP * SP + SP] = fma2(e[j], e[j], sum2[SP * SP + SP]);
+      }
+      {
+        P2 w[H];
+        p.w.load<V, ODD>(c, C - c, w);
+#pragma unroll
+        for (int j = 0; j < H; ++j) e[j] = mul2(e[j], w[j]);
+      }
+      if (gated) {
+        P2 slope[H];
+        gates<V, true>(p.act, g, slope);
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+          slope[j] = mul2(slope[j], mul2(e[j], dv[j]));
+          e[j] = mul2(e[j], g[j]);
+          dv[j] = mul2(dv[j], g[j]);
+        }
+        keep<V>(item + KB, lane, slope);
+      }
+      keep<V>(item, lane, dv);
+#pragma unroll
+      for (int i = 0; i < SP; ++i)
+#pragma unroll
+        for (int j = 0; j < H; ++j) sum2[SP * SP + i] = fma2(D[i][j], e[j], sum2[SP * SP + i]);
+    }
+    float sum[R], total[Sum::CH];
+#pragma unroll
+    for (int i = 0; i < R; ++i) sum[i] = both(sum2[i]);
+    Sum::run(sum, total, red, turn, G, group, lane, warp);
+    const float rho = p.norm ? rsqrtf(of_total(total, SP * SP + SP) * inv_c + p.eps) : 1.0f;
+    float gy = 0.0f;
+    {
+      P2 b[SP];
+      Co::read(co_s, Co::NP, b);
+#pragma unroll
+      for (int i = 0; i < SP; ++i) gy += low(b[i]) * of_total(total, SP * SP + i);
+    }
+    const float sr = p.scale * rho;
+    const P2 sr2 = twice(sr), minus_k = twice(p.norm ? -sr * gy * inv_c * rho * rho : 0.0f);
+    if (warp == 0) {
+#pragma unroll
+      for (int ch = 0; ch < Sum::CH; ++ch) {
+        const int n = ch * 32 + lane, i = n % SP, j = n / SP;
+        if (n < SP * SP) {
+          if (p.dP && i < S && j < S) put_any(p.dP, p.P.bf16, (int64_t(t) * S + i) * S + j, total[ch]);
+        } else if (n < SP * SP + S) {
+          if (p.db) put_any(p.db, p.b.bf16, int64_t(t) * S + n - SP * SP, sr * total[ch]);
+        }
+      }
+    }
+    TY* dy = p.dy ? static_cast<TY*>(p.dy) + uint64_t(t) * uint32_t(C) : nullptr;
+    TY* dgate = gated && p.dgate ? static_cast<TY*>(p.dgate) + uint64_t(t) * uint32_t(C) : nullptr;
+    item = item0;
+#pragma unroll 1
+    for (int c = l * V; c < C; c += GV, item += ITEM) {
+      P2 yv[H], w[H], d[H];
+      if (direct)
+        RY::load(y + c, yv, C - c);
+      else
+        RY::kept(item + E::KY, lane, yv);
+      if (dgate) {
+        P2 g[H];
+        kept<V>(item + KB, lane, g);
+#pragma unroll
+        for (int j = 0; j < H; ++j) g[j] = mul2(g[j], sr2);
+        RY::store(dgate + c, g, C - c);
+      }
+      p.w.load<V, ODD>(c, C - c, w);
+      kept<V>(item, lane, d);
+#pragma unroll
+      for (int j = 0; j < H; ++j) d[j] = mul2(d[j], sr2);
+      if (p.dw) add_share<V>(item + E::KW, lane, row_dw ? row_dw + c : nullptr, d, yv);
+      if (dy) {
+#pragma unroll
+        for (int j = 0; j < H; ++j) d[j] = fma2(d[j], w[j], mul2(minus_k, yv[j]));
+        RY::store(dy + c, d, C - c);
+      }
+    }
+  }
+  copy_wait_all();
+  if (!direct && (p.dw || (NEXT && p.dwn))) {
+    __syncthreads();
+    const int64_t row = int64_t(blockIdx.x) * pitch(C);
+    const char* first = smem + warp * p.warp_bytes + DEPTH * SLOT;
+    if (p.dw) sum_shares<V>(first + E::KW, p, NG, ITEM, p.dw + row);
+    if (NEXT && p.dwn) sum_shares<V>(first + E::KN, p, NG, ITEM, p.dwn + row);
+  }
+}
+
+template <bool NEXT>
+struct Backward {
+  const Params& p;
+  int* rows;
+  cudaStream_t s;
+  template <int SP, bool EXACT, class TX, class TY, int V, bool ODD>
+  cudaError_t operator()() const {
+    using E = LeaveBackward<SP, TX, TY, V, ODD, NEXT>;
+    Params q = p;
+    const bool mix = p.P.p != nullptr, gated = p.gate != nullptr;
+    const Shape sh = plan(q, shape_of(p.T, p.C, V, HCB_LEAVE_BWD_PER, 256), V, [&](int G, int direct) {
+      return Need{E::DEPTH * E::slot(mix, gated), E::item(gated, direct),
+                  4 * (G / 32 * E::Co::FLOATS + E::Sum::floats(G) + (NEXT ? E::SumNext::floats(G) : 0))};
+    });
+    const int most = p.dw || p.dwn ? kMaxRows : 1 << 30;
+    if (EXACT && !q.direct && mix == (SP > 1)) {
+      if (gated) return launch<leave_backward_kernel<SP, EXACT, TX, TY, V, ODD, NEXT, EXACT ? 1 : 2>>(q, sh, most, rows, s);
+      return launch<leave_backward_kernel<SP, EXACT, TX, TY, V, ODD, NEXT, EXACT ? 0 : 2>>(q, sh, most, rows, s);
+    }
+    return launch<leave_backward_kernel<SP, false, TX, TY, V, ODD, NEXT, 2>>(q, sh, most, rows, s);
+  }
+};
+
+}  // namespace hcb
