@@ -103,6 +103,19 @@ __device__ __forceinline__ P2 add2(P2 a, P2 b) {
   return r;
 }
 
+// Two pairs from and to 16 bytes (as float4: the compiler splits accesses of
+// two 64-bit integers, and the halves then conflict in shared memory).
+__device__ __forceinline__ void get16(const void* p, P2& a, P2& b) {
+  const float4 q = *static_cast<const float4*>(p);
+  a = pair(q.x, q.y), b = pair(q.z, q.w);
+}
+__device__ __forceinline__ void put16(void* p, P2 a, P2 b) {
+  float4 q;
+  split(a, q.x, q.y);
+  split(b, q.z, q.w);
+  *static_cast<float4*>(p) = q;
+}
+
 __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -279,16 +292,12 @@ constexpr int kFloats = 128 * V;  // bytes of a warp
 template <int V, int PLANE = 512>
 __device__ __forceinline__ void keep(char* s, int lane, const P2 (&v)[V / 2]) {
 #pragma unroll
-  for (int i = 0; i < V / 4; ++i)
-    *reinterpret_cast<ulonglong2*>(s + lane * 16 + i * PLANE) = make_ulonglong2(v[2 * i], v[2 * i + 1]);
+  for (int i = 0; i < V / 4; ++i) put16(s + lane * 16 + i * PLANE, v[2 * i], v[2 * i + 1]);
 }
 template <int V, int PLANE = 512>
 __device__ __forceinline__ void kept(const char* s, int lane, P2 (&v)[V / 2]) {
 #pragma unroll
-  for (int i = 0; i < V / 4; ++i) {
-    const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(s + lane * 16 + i * PLANE);
-    v[2 * i] = q.x, v[2 * i + 1] = q.y;
-  }
+  for (int i = 0; i < V / 4; ++i) get16(s + lane * 16 + i * PLANE, v[2 * i], v[2 * i + 1]);
 }
 
 // Add a b to a thread's share of a weight gradient: in shared memory at s,
@@ -336,10 +345,7 @@ struct Any {
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < V / 4; ++k) {
-        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(static_cast<const float*>(p) + i + 4 * k);
-        v[2 * k] = q.x, v[2 * k + 1] = q.y;
-      }
+      for (int k = 0; k < V / 4; ++k) get16(static_cast<const float*>(p) + i + 4 * k, v[2 * k], v[2 * k + 1]);
     }
   }
 };
@@ -461,10 +467,7 @@ struct Coefficients {
   __device__ __forceinline__ static void read(const float* s, int from, P2 (&v)[SP]) {
     if constexpr (SP >= 2) {
 #pragma unroll
-      for (int i = 0; i < SP; i += 2) {
-        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(s + 2 * (from + i));
-        v[i] = q.x, v[i + 1] = q.y;
-      }
+      for (int i = 0; i < SP; i += 2) get16(s + 2 * (from + i), v[i], v[i + 1]);
     } else {
       v[0] = *reinterpret_cast<const P2*>(s + 2 * from);
     }

@@ -36,6 +36,8 @@ struct LeaveBackward {
   using Co = Coefficients<SP, true, true, NEXT, true>;
   // the sums: dP (by column), <D_i, e>, <y, y>
   static constexpr int R = SP * SP + SP + 1;
+  // dP's sums as pairs of channels, where the registers hold twice as many
+  static constexpr bool PAIRS = SP <= 2 || (SP == 4 && V == 4);
   using Sum = GroupSum<R>;
   using SumNext = GroupSum<2 * SP>;
   static constexpr int DEPTH = HCB_LEAVE_BWD_DEPTH;
@@ -209,7 +211,8 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
     const TX* x = at_row<TX>(p.x, t, p.x_ts);
     const TY* y = at_row<TY>(p.y, t, p.y_ts);
     const TY* gate = at_row<TY>(p.gate, t, p.gate_ts);
-    P2 sum2[R] = {};
+    P2 sum_dP2[E::PAIRS ? SP * SP : 1] = {}, sum_e2[SP] = {}, sum_y2 = 0;
+    float sum_dP[E::PAIRS ? 1 : SP * SP] = {};
     TX* dx = p.dx ? static_cast<TX*>(p.dx) + uint64_t(t) * uint32_t(S * C) : nullptr;
     char* item = item0;
 #pragma unroll 1
@@ -263,7 +266,16 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
 #pragma unroll
             for (int i = 0; i < SP; ++i)
 #pragma unroll
-              for (int j = 0; j < H; ++j) sum2[q * SP + i] = fma2(D[i][j], xv[j], sum2[q * SP + i]);
+              for (int j = 0; j < H; ++j) {
+                if constexpr (E::PAIRS) {
+                  sum_dP2[q * SP + i] = fma2(D[i][j], xv[j], sum_dP2[q * SP + i]);
+                } else {
+                  float dl, dh, xl, xh;
+                  split(D[i][j], dl, dh);
+                  split(xv[j], xl, xh);
+                  sum_dP[q * SP + i] = fmaf(dh, xh, fmaf(dl, xl, sum_dP[q * SP + i]));
+                }
+              }
           }
         }
       }
@@ -301,7 +313,7 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
         dv[j] = mul2(b[0], D[0][j]);
 #pragma unroll
         for (int i = 1; i < SP; ++i) dv[j] = fma2(b[i], D[i][j], dv[j]);
-        sum2[SP * SP + SP] = fma2(e[j], e[j], sum2[SP * SP + SP]);
+        sum_y2 = fma2(e[j], e[j], sum_y2);
       }
       {
         P2 w[H];
@@ -324,11 +336,14 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
 #pragma unroll
       for (int i = 0; i < SP; ++i)
 #pragma unroll
-        for (int j = 0; j < H; ++j) sum2[SP * SP + i] = fma2(D[i][j], e[j], sum2[SP * SP + i]);
+        for (int j = 0; j < H; ++j) sum_e2[i] = fma2(D[i][j], e[j], sum_e2[i]);
     }
     float sum[R], total[Sum::CH];
 #pragma unroll
-    for (int i = 0; i < R; ++i) sum[i] = both(sum2[i]);
+    for (int i = 0; i < SP * SP; ++i) sum[i] = E::PAIRS ? both(sum_dP2[E::PAIRS ? i : 0]) : sum_dP[E::PAIRS ? 0 : i];
+#pragma unroll
+    for (int i = 0; i < SP; ++i) sum[SP * SP + i] = both(sum_e2[i]);
+    sum[SP * SP + SP] = both(sum_y2);
     Sum::run(sum, total, red, turn, G, group, lane, warp);
     const float rho = p.norm ? rsqrtf(of_total(total, SP * SP + SP) * inv_c + p.eps) : 1.0f;
     float gy = 0.0f;
