@@ -324,20 +324,23 @@ __device__ __forceinline__ void add_share(char* s, int lane, float* g, const P2 
 struct Any {
   const void* p;
   int32_t bf16;
-  __device__ __forceinline__ float at(int64_t i) const {
+  __device__ __forceinline__ float at(int i) const {
     return bf16 ? b4::bf16lo(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
   }
   // Elements [i, i + V), 1 where there are none (left: elements from i on).
-  template <int V, bool ODD>
+  // W says what is known of them: nothing (0), or that they are there, on 16
+  // bytes, and fp32 (1) or bf16 (2).  Told apart at run time, both types'
+  // loads, conversions and choices between them are issued every time.
+  template <int V, bool ODD, int W>
   __device__ __forceinline__ void load(int i, int left, P2 (&v)[V / 2]) const {
-    if (p == nullptr) {
+    if (W == 0 && p == nullptr) {
 #pragma unroll
       for (int k = 0; k < V / 2; ++k) v[k] = twice(1.0f);
-    } else if constexpr (ODD) {
+    } else if (ODD && (W == 0 || left < V)) {
 #pragma unroll
       for (int k = 0; k < V / 2; ++k)
         v[k] = pair(2 * k < left ? at(i + 2 * k) : 0.0f, 2 * k + 1 < left ? at(i + 2 * k + 1) : 0.0f);
-    } else if (bf16) {
+    } else if (W == 2 || (W == 0 && bf16)) {
 #pragma unroll
       for (int k = 0; k < V / 4; ++k) {
         const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i + 4 * k);
@@ -348,6 +351,15 @@ struct Any {
       for (int k = 0; k < V / 4; ++k) get16(static_cast<const float*>(p) + i + 4 * k, v[2 * k], v[2 * k + 1]);
     }
   }
+};
+
+// What W above a pass's weights (null where it has no such weight) allow: the
+// type that both have, 0 where they differ, are missing or off 16 bytes.
+struct Weights {
+  static int kind(const Any& w) {
+    return w.p == nullptr || (reinterpret_cast<uintptr_t>(w.p) & 15) != 0 ? 0 : w.bf16 ? 2 : 1;
+  }
+  static int kind(const Any& w, const Any& wn) { return kind(w) == kind(wn) ? kind(w) : 0; }
 };
 
 __device__ __forceinline__ void put_any(void* p, int32_t bf16, int64_t i, float v) {

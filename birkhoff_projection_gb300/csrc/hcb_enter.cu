@@ -33,7 +33,7 @@ struct Enter {
   }
 };
 
-template <int SP, bool EXACT, class TX, class TY, int V, bool ODD>
+template <int SP, bool EXACT, class TX, class TY, int V, bool ODD, int W>
 __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
   using E = Enter<SP, TX, TY, V, ODD>;
   using RX = typename E::RX;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
     for (int c = l * V; c < C; c += GV, item += E::ITEM) {
       P2 u[H], w[H];
       kept<V>(item, lane, u);
-      p.w.load<V, ODD>(c, C - c, w);
+      p.w.load<V, ODD, W>(c, C - c, w);
 #pragma unroll
       for (int j = 0; j < H; ++j) u[j] = mul2(u[j], mul2(r, w[j]));
       RY::store(h + c, u, C - c);
@@ -148,7 +148,7 @@ struct EnterBackward {
   }
 };
 
-template <int SP, bool EXACT, class TX, class TY, int V, bool ODD>
+template <int SP, bool EXACT, class TX, class TY, int V, bool ODD, int W>
 __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Params p) {
   using E = EnterBackward<SP, TX, TY, V, ODD>;
   using RX = typename E::RX;
@@ -230,10 +230,11 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
     char* item = item0;
 #pragma unroll 1
     for (int c = l * V, k = 0; k < K; ++k, c += GV, item += ITEM) {
+      P2 w[H];
+      if (c < C) p.w.load<V, ODD, W>(c, C - c, w);
       copy_wait<DEPTH - 1>();
       if (c < C) {
-        P2 xv[SP][H], g[H], w[H], u[H] = {};
-        p.w.load<V, ODD>(c, C - c, w);
+        P2 xv[SP][H], g[H], u[H] = {};
 #pragma unroll
         for (int i = 0; i < SP; ++i) {
           if (EXACT || i < S) {
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
         P2 u[H], g[H], w[H];
         kept<V>(item, lane, u);
         RY::kept(item + E::KH, lane, g);
-        p.w.load<V, ODD>(c, C - c, w);
+        p.w.load<V, ODD, W>(c, C - c, w);
 #pragma unroll
         for (int j = 0; j < H; ++j) u[j] = mul2(r2, u[j]);
         if (p.dw) add_share<V>(item + E::KW, lane, row_dw ? row_dw + c : nullptr, g, u);
@@ -331,7 +332,10 @@ struct Forward {
     Params q = p;
     int grid;
     const Shape sh = plan(q, shape_of(p.T, p.C, V, HCB_ENTER_PER, kMaxGroup), V, Enter<SP, TX, TY, V, ODD>::need);
-    return launch<enter_kernel<SP, EXACT, TX, TY, V, ODD>>(q, sh, 1 << 30, &grid, s);
+    const int w = EXACT ? Weights::kind(p.w) : 0;
+    if (w == 1) return launch<enter_kernel<SP, EXACT, TX, TY, V, ODD, EXACT ? 1 : 0>>(q, sh, 1 << 30, &grid, s);
+    if (w == 2 && !ODD) return launch<enter_kernel<SP, EXACT && !ODD, TX, TY, V, ODD, EXACT && !ODD ? 2 : 0>>(q, sh, 1 << 30, &grid, s);
+    return launch<enter_kernel<SP, false, TX, TY, V, ODD, 0>>(q, sh, 1 << 30, &grid, s);
   }
 };
 struct Backward {
@@ -344,8 +348,11 @@ struct Backward {
     const Shape sh =
         plan(q, shape_of(p.T, p.C, V, HCB_ENTER_BWD_PER, kMaxGroup), V, EnterBackward<SP, TX, TY, V, ODD>::need);
     const int most = p.dw ? kMaxRows : 1 << 30;
-    if (EXACT && !q.direct) return launch<enter_backward_kernel<SP, EXACT, TX, TY, V, ODD>>(q, sh, most, rows, s);
-    return launch<enter_backward_kernel<SP, false, TX, TY, V, ODD>>(q, sh, most, rows, s);
+    const int w = EXACT && !q.direct ? Weights::kind(p.w) : 0;
+    if (w == 1) return launch<enter_backward_kernel<SP, EXACT, TX, TY, V, ODD, EXACT ? 1 : 0>>(q, sh, most, rows, s);
+    if (w == 2 && !ODD)
+      return launch<enter_backward_kernel<SP, EXACT && !ODD, TX, TY, V, ODD, EXACT && !ODD ? 2 : 0>>(q, sh, most, rows, s);
+    return launch<enter_backward_kernel<SP, false, TX, TY, V, ODD, 0>>(q, sh, most, rows, s);
   }
 };
 

@@ -32,7 +32,7 @@ struct Leave {
   }
 };
 
-template <int SP, bool EXACT, class TX, class TY, int V, bool ODD>
+template <int SP, bool EXACT, class TX, class TY, int V, bool ODD, int W>
 __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(const Params p) {
   using E = Leave<SP, TX, TY, V, ODD>;
   using RX = typename E::RX;
@@ -99,10 +99,11 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
     char* item = item0;
 #pragma unroll 1
     for (int c = l * V, k = 0; k < K; ++k, c += GV, item += E::ITEM) {
+      P2 w[H];
+      if (c < C) p.w.load<V, ODD, W>(c, C - c, w);
       copy_wait<DEPTH - 1>();
       if (c < C) {
-        P2 v[H], w[H];
-        p.w.load<V, ODD>(c, C - c, w);
+        P2 v[H];
         RY::arrived(slot + E::Y, lane, y + c, v);
 #pragma unroll
         for (int j = 0; j < H; ++j) {
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
       for (int c = l * V; c < C; c += GV, item += E::ITEM) {
         P2 u[H], w[H];
         kept<V>(item, lane, u);
-        p.wn.load<V, ODD>(c, C - c, w);
+        p.wn.load<V, ODD, W>(c, C - c, w);
 #pragma unroll
         for (int j = 0; j < H; ++j) u[j] = mul2(u[j], mul2(r, w[j]));
         RY::store(h + c, u, C - c);
@@ -219,9 +220,10 @@ struct Forward {
     int grid;
     const Shape sh =
         plan(q, shape_of(p.T, p.C, V, HCB_LEAVE_PER, SP == 8 ? 256 : kMaxGroup), V, Leave<SP, TX, TY, V, ODD>::need);
-    if (EXACT && (p.P.p != nullptr) == (SP > 1))
-      return launch<leave_kernel<SP, EXACT, TX, TY, V, ODD>>(q, sh, 1 << 30, &grid, s);
-    return launch<leave_kernel<SP, false, TX, TY, V, ODD>>(q, sh, 1 << 30, &grid, s);
+    const int w = EXACT && (p.P.p != nullptr) == (SP > 1) ? Weights::kind(p.w, p.h ? p.wn : p.w) : 0;
+    if (w == 1) return launch<leave_kernel<SP, EXACT, TX, TY, V, ODD, EXACT ? 1 : 0>>(q, sh, 1 << 30, &grid, s);
+    if (w == 2 && !ODD) return launch<leave_kernel<SP, EXACT && !ODD, TX, TY, V, ODD, EXACT && !ODD ? 2 : 0>>(q, sh, 1 << 30, &grid, s);
+    return launch<leave_kernel<SP, false, TX, TY, V, ODD, 0>>(q, sh, 1 << 30, &grid, s);
   }
 };
 

@@ -11,9 +11,6 @@
 #ifndef HCB_LEAVE_BWD_MINB1
 #define HCB_LEAVE_BWD_MINB1 3
 #endif
-#ifndef HCB_LEAVE_BWD_MINB2
-#define HCB_LEAVE_BWD_MINB2 2
-#endif
 #ifndef HCB_LEAVE_BWD_PER
 #define HCB_LEAVE_BWD_PER 2
 #endif
@@ -41,7 +38,8 @@ struct LeaveBackward {
   using Sum = GroupSum<R>;
   using SumNext = GroupSum<2 * SP>;
   static constexpr int DEPTH = HCB_LEAVE_BWD_DEPTH;
-  static constexpr int MINB = SP == 1 ? HCB_LEAVE_BWD_MINB1 : SP == 2 ? HCB_LEAVE_BWD_MINB2 : SP == 4 ? 2 : 1;
+  // CTAs that the registers have to leave room for on an SM
+  static constexpr int minb(int gate) { return SP == 1 && gate == 0 ? HCB_LEAVE_BWD_MINB1 : SP <= 4 ? 2 : 1; }
   // a slot: dout, y, gate and x; or the stored result, and dh where y would be
   static constexpr int Y = SP * RX::SLOT, GATE = Y + RY::SLOT, X = GATE + RY::SLOT;
   __host__ __device__ static constexpr int slot(bool mix, bool gated) {
@@ -56,8 +54,8 @@ struct LeaveBackward {
 };
 
 // GATE: 0 no gate, 1 a gate, 2 told at run time.
-template <int SP, bool EXACT, class TX, class TY, int V, bool ODD, bool NEXT, int GATE>
-__global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::MINB) leave_backward_kernel(const Params p) {
+template <int SP, bool EXACT, class TX, class TY, int V, bool ODD, bool NEXT, int GATE, int W>
+__global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::minb(GATE)) leave_backward_kernel(const Params p) {
   using E = LeaveBackward<SP, TX, TY, V, ODD, NEXT>;
   using RX = typename E::RX;
   using RY = typename E::RY;
@@ -156,10 +154,11 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
       char* item = item0;
 #pragma unroll 1
       for (int c = l * V, k = 0; k < K; ++k, c += GV, item += ITEM) {
+        P2 w[H];
+        if (c < C) p.wn.load<V, ODD, W>(c, C - c, w);
         copy_wait<DEPTH - 1>();
         if (c < C) {
-          P2 xv[SP][H], g[H], w[H], u[H] = {};
-          p.wn.load<V, ODD>(c, C - c, w);
+          P2 xv[SP][H], g[H], u[H] = {};
 #pragma unroll
           for (int i = 0; i < SP; ++i) {
             if (EXACT || i < S) {
@@ -226,7 +225,7 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
           RY::load(at_row<TY>(p.dh, t, p.dh_ts) + c, h, C - c);
         else
           RY::kept(item + E::KH, lane, h);
-        p.wn.load<V, ODD>(c, C - c, wn);
+        p.wn.load<V, ODD, W>(c, C - c, wn);
 #pragma unroll
         for (int j = 0; j < H; ++j) du[j] = mul2(r2, du[j]);
         if (p.dwn) add_share<V>(item + E::KN, lane, row_dwn ? row_dwn + c : nullptr, h, du);
@@ -317,7 +316,7 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
       }
       {
         P2 w[H];
-        p.w.load<V, ODD>(c, C - c, w);
+        p.w.load<V, ODD, W>(c, C - c, w);
 #pragma unroll
         for (int j = 0; j < H; ++j) e[j] = mul2(e[j], w[j]);
       }
@@ -383,7 +382,7 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
         for (int j = 0; j < H; ++j) g[j] = mul2(g[j], sr2);
         RY::store(dgate + c, g, C - c);
       }
-      p.w.load<V, ODD>(c, C - c, w);
+      p.w.load<V, ODD, W>(c, C - c, w);
       kept<V>(item, lane, d);
 #pragma unroll
       for (int j = 0; j < H; ++j) d[j] = mul2(d[j], sr2);
@@ -420,11 +419,17 @@ struct Backward {
                   4 * (G / 32 * E::Co::FLOATS + E::Sum::floats(G) + (NEXT ? E::SumNext::floats(G) : 0))};
     });
     const int most = p.dw || p.dwn ? kMaxRows : 1 << 30;
-    if (EXACT && !q.direct && mix == (SP > 1)) {
-      if (gated) return launch<leave_backward_kernel<SP, EXACT, TX, TY, V, ODD, NEXT, EXACT ? 1 : 2>>(q, sh, most, rows, s);
-      return launch<leave_backward_kernel<SP, EXACT, TX, TY, V, ODD, NEXT, EXACT ? 0 : 2>>(q, sh, most, rows, s);
-    }
-    return launch<leave_backward_kernel<SP, false, TX, TY, V, ODD, NEXT, 2>>(q, sh, most, rows, s);
+    const int w = EXACT && !q.direct && mix == (SP > 1) ? Weights::kind(p.w, NEXT ? p.wn : p.w) : 0;
+    constexpr int W1 = EXACT ? 1 : 0, W2 = EXACT && !ODD ? 2 : 0;
+    if (w == 1 && gated)
+      return launch<leave_backward_kernel<SP, EXACT, TX, TY, V, ODD, NEXT, W1 ? 1 : 2, W1>>(q, sh, most, rows, s);
+    if (w == 1)
+      return launch<leave_backward_kernel<SP, EXACT, TX, TY, V, ODD, NEXT, W1 ? 0 : 2, W1>>(q, sh, most, rows, s);
+    if (w == 2 && W2 && gated)
+      return launch<leave_backward_kernel<SP, W2 != 0, TX, TY, V, ODD, NEXT, W2 ? 1 : 2, W2>>(q, sh, most, rows, s);
+    if (w == 2 && W2)
+      return launch<leave_backward_kernel<SP, W2 != 0, TX, TY, V, ODD, NEXT, W2 ? 0 : 2, W2>>(q, sh, most, rows, s);
+    return launch<leave_backward_kernel<SP, false, TX, TY, V, ODD, NEXT, 2, 0>>(q, sh, most, rows, s);
   }
 };
 
