@@ -5,9 +5,12 @@
 //
 // Mapping.  A group of G threads (a power of two, a warp at least) takes one
 // token at a time; a CTA holds NG groups, and the grid is persistent (SMs x
-// resident CTAs).  Thread l of a group owns the channels [(k G + l) V, + V)
-// of every token, k = 0 .. K - 1, where V elements are 16 bytes of the wider
-// row type.
+// resident CTAs).  A warp owns the same blocks of 32 V channels of every
+// token, k = 0 .. K - 1, where V elements are 16 bytes of the wider row type.
+// Where rows allow vectors, lane l has the V channels from l V on in a block;
+// where they do not (ODD), it has the pairs of channels 64 i + 2 l, so that a
+// warp's accesses of 4 bytes are to neighbouring words (with V channels to a
+// lane they were 16 bytes apart, and leave at 5001 x 4 x 1001 took 41 us).
 //
 // Loads.  All of these kernels are bound by memory, and a row's sums keep a
 // group waiting at a barrier; loads into registers then left the memory idle
@@ -54,16 +57,6 @@ constexpr int kThreads = 256;   // threads of a CTA with many short rows
 constexpr int kMaxGroup = 512;  // threads of a group at most (16 warps: GroupSum)
 constexpr int kMaxRows = 640;   // CTAs of a backward pass at most (rows of partial weight gradients)
 
-// ---------------------------------------------------------------------------
-// V consecutive elements of a row, and their way through shared memory.
-//
-// ODD rows need not lie on 16-byte boundaries (any alignment of the element
-// type): they are copied in 4-byte words, of which a bf16 row that begins in
-// the middle of a word takes one more, and end with C wherever that is
-// (`left` elements from here).  The word around a row's first element is read
-// whole; no allocation begins inside a word.  Past the row's last element
-// nothing is read (the copy's source size) and the slot holds zeros.
-// ---------------------------------------------------------------------------
 // Two floats of neighbouring channels, for the packed fp32 instructions
 // (fma.rn.f32x2 and so on: the same roundings as one by one, half the issue
 // slots; the kernels are near the issue limit).
@@ -116,6 +109,32 @@ __device__ __forceinline__ void put16(void* p, P2 a, P2 b) {
   *static_cast<float4*>(p) = q;
 }
 
+// ---------------------------------------------------------------------------
+// A lane's V elements of a block of a row, and their way through shared
+// memory.  `row` is the row's first element and c the lane's first channel
+// (ODD: the block's), below C.
+//
+// ODD rows need not lie on 16-byte boundaries (any alignment of the element
+// type) and end with C wherever that is.  They are copied in 4-byte words.
+// Where a bf16 block begins in the middle of a word, that word is read whole
+// (no allocation begins inside a word) and a pair is the upper half of one
+// word and the lower half of the next; past the row's last element nothing is
+// read (the copy's source size), and the slot holds zeros.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void copy4(uint32_t d, const void* p) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(p) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t d, const void* p) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(p) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t d, const void* p) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(p) : "memory");
+}
+// n of 4 bytes, the rest zero; p is not read if n <= 0 but has to be valid
+__device__ __forceinline__ void copy4_of(uint32_t d, const void* p, const void* valid, int n) {
+  n = max(0, min(4, n));
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(n > 0 ? p : valid), "r"(n) : "memory");
+}
 __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -127,49 +146,65 @@ template <class T, int V, bool ODD>
 struct Row {
   static constexpr int H = V / 2;
   static constexpr int BYTES = V * static_cast<int>(sizeof(T));
-  static constexpr int WORDS = BYTES / 4 + (ODD && sizeof(T) == 2 ? 1 : 0);
-  static constexpr int SLOT = 32 * 4 * WORDS;  // bytes of a warp in a slot
-  static constexpr int KEPT = 32 * BYTES;      // and of what it keeps in this type
+  static constexpr bool SPLIT = ODD && sizeof(T) == 2;               // pairs may straddle words
+  static constexpr int SLOT = 32 * BYTES + (SPLIT ? 16 : 0);         // bytes of a warp in a slot
+  static constexpr int KEPT = 32 * BYTES;                            // and of what it keeps in this type
   static_assert(BYTES == 16 || BYTES == 8, "");
 
-  // Begin the copy of p[0, min(V, left)) into the lane's part of the slot at s.
-  __device__ __forceinline__ static void copy(char* s, int lane, const T* p, int left) {
-    const uint32_t d = b4::smem_addr(s + lane * (ODD ? 4 : BYTES));
+  __device__ __forceinline__ static int straddles(const T* row, int c) {
+    return SPLIT ? static_cast<int>(reinterpret_cast<uintptr_t>(row + c) & 2) : 0;
+  }
+  // Begin the copy of the lane's elements into the slot at s.
+  __device__ __forceinline__ static void copy(char* s, int lane, const T* row, int c, int C) {
     if constexpr (!ODD) {
+      const uint32_t d = b4::smem_addr(s + lane * BYTES);
       if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(p) : "memory");
+        copy16(d, row + c);
       else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(p) : "memory");
-    } else {
-      const int before = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 3);  // 0, or 2 for bf16
-      const char* q = reinterpret_cast<const char*>(p) - before;
-      if (left >= V + 2) {  // all words lie within the row
+        copy8(d, row + c);
+    } else if constexpr (SPLIT) {
+      const int before = straddles(row, c);
+      const char* block = reinterpret_cast<const char*>(row + c) - before;
+      const char* p = block + 4 * lane;
+      const uint32_t d = b4::smem_addr(s + 4 * lane);
+      if (c + 32 * V + 2 <= C) {  // all of its words lie within the row
 #pragma unroll
-        for (int w = 0; w < WORDS; ++w)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d + 128 * w), "l"(q + 4 * w)
-                       : "memory");
+        for (int i = 0; i < H; ++i) copy4(d + 128 * i, p + 128 * i);
+        if (before && lane == 31) copy4(d + 128 * (H - 1) + 4, p + 128 * (H - 1) + 4);
       } else {
-        const int end = before + min(left, V) * static_cast<int>(sizeof(T));
+        const int end = 2 * (C - c) + before - 4 * lane;  // bytes from p to the row's end
 #pragma unroll
-        for (int w = 0; w < WORDS; ++w) {
-          const int n = max(0, min(4, end - 4 * w));
-          const char* src = n > 0 ? q + 4 * w : q;  // in bounds even where nothing is read
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d + 128 * w), "l"(src), "r"(n)
-                       : "memory");
+        for (int i = 0; i < H; ++i) copy4_of(d + 128 * i, p + 128 * i, block, end - 128 * i);
+        if (before && lane == 31)
+          copy4_of(d + 128 * (H - 1) + 4, p + 128 * (H - 1) + 4, block, end - 128 * (H - 1) - 4);
+      }
+    } else {
+      const T* p = row + c + 2 * lane;
+      const uint32_t d = b4::smem_addr(s + 8 * lane);
+      if (c + 32 * V <= C && (reinterpret_cast<uintptr_t>(p) & 7) == 0) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) copy8(d + 256 * i, p + 64 * i);
+      } else {
+        const int end = 4 * (C - c - 2 * lane);
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+          copy4_of(d + 256 * i, p + 64 * i, row, end - 256 * i);
+          copy4_of(d + 256 * i + 4, p + 64 * i + 1, row, end - 256 * i - 4);
         }
       }
     }
   }
-  // The arrived slot's elements (p: where they came from, for its alignment).
-  __device__ __forceinline__ static void arrived(const char* s, int lane, const T* p, P2 (&v)[H]) {
+  // The arrived slot's elements.
+  __device__ __forceinline__ static void arrived(const char* s, int lane, const T* row, int c, P2 (&v)[H]) {
     uint32_t w[BYTES / 4];
-    raw(s, lane, p, w);
+    raw(s, lane, row, c, w);
     unpack(w, v);
   }
   // The same, and kept as they are at `to`.
-  __device__ __forceinline__ static void arrived_kept(const char* s, int lane, const T* p, P2 (&v)[H], char* to) {
+  __device__ __forceinline__ static void arrived_kept(const char* s, int lane, const T* row, int c, P2 (&v)[H],
+                                                      char* to) {
     uint32_t w[BYTES / 4];
-    raw(s, lane, p, w);
+    raw(s, lane, row, c, w);
     unpack(w, v);
     if constexpr (BYTES == 16)
       *reinterpret_cast<uint4*>(to + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -181,51 +216,56 @@ struct Row {
     words(s + lane * BYTES, w);
     unpack(w, v);
   }
-  // p[0, min(V, left)) read directly, zeros behind.
-  __device__ __forceinline__ static void load(const T* p, P2 (&v)[H], int left) {
+  // The lane's elements read directly, zeros past C.
+  __device__ __forceinline__ static void load(const T* row, int c, int lane, int C, P2 (&v)[H]) {
     if constexpr (ODD) {
-      float x[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        x[i] = 0.0f;
-        if (i < left) {
-          if constexpr (sizeof(T) == 4)
-            x[i] = p[i];
-          else
-            x[i] = b4::bf16lo(p[i].bits);
-        }
+      for (int i = 0; i < H; ++i) {
+        const int e = c + 64 * i + 2 * lane;
+        v[i] = pair(e < C ? value(row + e) : 0.0f, e + 1 < C ? value(row + e + 1) : 0.0f);
       }
-#pragma unroll
-      for (int i = 0; i < H; ++i) v[i] = pair(x[2 * i], x[2 * i + 1]);
     } else {
       uint32_t w[BYTES / 4];
-      words(reinterpret_cast<const char*>(p), w);
+      words(reinterpret_cast<const char*>(row + c), w);
       unpack(w, v);
     }
   }
-  // Round and write v to p[0, min(V, left)); v becomes what was written.
-  __device__ __forceinline__ static void store_rounded(T* p, P2 (&v)[H], int left) {
+  // Round and write v; store_rounded leaves in v what was written.
+  __device__ __forceinline__ static void store(T* row, int c, int lane, int C, const P2 (&v)[H]) {
     uint32_t w[BYTES / 4];
     pack(v, w);
-    put(p, w, left);
-    if constexpr (sizeof(T) == 2) unpack(w, v);
+    put(row, c, lane, C, w);
   }
-  __device__ __forceinline__ static void store(T* p, const P2 (&v)[H], int left) {
+  __device__ __forceinline__ static void store_rounded(T* row, int c, int lane, int C, P2 (&v)[H]) {
     uint32_t w[BYTES / 4];
     pack(v, w);
-    put(p, w, left);
+    put(row, c, lane, C, w);
+    if constexpr (sizeof(T) == 2) unpack(w, v);
   }
 
  private:
-  __device__ __forceinline__ static void raw(const char* s, int lane, const T* p, uint32_t (&w)[BYTES / 4]) {
-    if constexpr (ODD) {
-      uint32_t q[WORDS];
+  __device__ __forceinline__ static float value(const T* p) {
+    if constexpr (sizeof(T) == 4)
+      return *p;
+    else
+      return b4::bf16lo(p->bits);
+  }
+  __device__ __forceinline__ static void raw(const char* s, int lane, const T* row, int c, uint32_t (&w)[BYTES / 4]) {
+    if constexpr (SPLIT) {
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(s) + lane;
+      if (straddles(row, c)) {
 #pragma unroll
-      for (int i = 0; i < WORDS; ++i) q[i] = *reinterpret_cast<const uint32_t*>(s + 128 * i + 4 * lane);
-      const uint32_t shift = (reinterpret_cast<uintptr_t>(p) & 3) * 8;
+        for (int i = 0; i < H; ++i) w[i] = __byte_perm(q[32 * i], q[32 * i + 1], 0x5432);
+      } else {
 #pragma unroll
-      for (int i = 0; i < BYTES / 4; ++i)
-        w[i] = sizeof(T) == 4 ? q[i] : __funnelshift_r(q[i], q[i + 1 < WORDS ? i + 1 : i], shift);
+        for (int i = 0; i < H; ++i) w[i] = q[32 * i];
+      }
+    } else if constexpr (ODD) {
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        const uint2 q = *reinterpret_cast<const uint2*>(s + 256 * i + 8 * lane);
+        w[(2 * i) % (BYTES / 4)] = q.x, w[(2 * i + 1) % (BYTES / 4)] = q.y;
+      }
     } else {
       words(s + lane * BYTES, w);
     }
@@ -256,66 +296,114 @@ struct Row {
         w[i] = b4::pack_bf16(lo, hi);
     }
   }
-  __device__ __forceinline__ static void put(T* p, const uint32_t (&w)[BYTES / 4], int left) {
+  __device__ __forceinline__ static void put(T* row, int c, int lane, int C, const uint32_t (&w)[BYTES / 4]) {
     if constexpr (!ODD) {
       if constexpr (BYTES == 16)
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
       else
-        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    } else if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
+    } else if constexpr (SPLIT) {
+      uint16_t* p = reinterpret_cast<uint16_t*>(row + c + 2 * lane);
+      const bool whole = c + 32 * V <= C;
+      if (whole && !straddles(row, c)) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i < left) p[i] = __uint_as_float(w[i]);
-    } else {
-      uint16_t* e = reinterpret_cast<uint16_t*>(p);
-      if (left < V) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (i < left) e[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
-      } else if ((reinterpret_cast<uintptr_t>(p) & 3) == 0) {
-#pragma unroll
-        for (int i = 0; i < H; ++i) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+        for (int i = 0; i < H; ++i) reinterpret_cast<uint32_t*>(p)[32 * i] = w[i];
       } else {
-        e[0] = static_cast<uint16_t>(w[0]);
+        const int left = whole ? 32 * V : C - c - 2 * lane;
 #pragma unroll
-        for (int i = 0; i < H - 1; ++i)
-          reinterpret_cast<uint32_t*>(e + 1)[i] = __funnelshift_r(w[i], w[i + 1], 16);
-        e[V - 1] = static_cast<uint16_t>(w[H - 1] >> 16);
+        for (int i = 0; i < H; ++i) {
+          if (64 * i < left) p[64 * i] = static_cast<uint16_t>(w[i]);
+          if (64 * i + 1 < left) p[64 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
+        }
+      }
+    } else {
+      uint32_t* p = reinterpret_cast<uint32_t*>(row + c + 2 * lane);
+      if (c + 32 * V <= C && (reinterpret_cast<uintptr_t>(p) & 7) == 0) {
+#pragma unroll
+        for (int i = 0; i < H; ++i)
+          *reinterpret_cast<uint2*>(p + 64 * i) = make_uint2(w[(2 * i) % (BYTES / 4)], w[(2 * i + 1) % (BYTES / 4)]);
+      } else {
+        const int left = C - c - 2 * lane;
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+          if (64 * i < left) p[64 * i] = w[(2 * i) % (BYTES / 4)];
+          if (64 * i + 1 < left) p[64 * i + 1] = w[(2 * i + 1) % (BYTES / 4)];
+        }
       }
     }
   }
 };
 
+// The oldest of DEPTH copies has arrived; a slot has been read and may be
+// copied to again.  A lane of an ODD kernel reads a word of its neighbour's,
+// so there the warp waits for each other (all of its branches are the warp's).
+template <int DEPTH, bool ODD>
+__device__ __forceinline__ void slot_ready() {
+  copy_wait<DEPTH - 1>();
+  if constexpr (ODD) __syncwarp();
+}
+template <bool ODD>
+__device__ __forceinline__ void slot_read() {
+  if constexpr (ODD) __syncwarp();
+}
+
 // V floats that a thread keeps for itself, in its warp's planes of four.
 template <int V>
 constexpr int kFloats = 128 * V;  // bytes of a warp
-template <int V, int PLANE = 512>
+template <int V>
 __device__ __forceinline__ void keep(char* s, int lane, const P2 (&v)[V / 2]) {
 #pragma unroll
-  for (int i = 0; i < V / 4; ++i) put16(s + lane * 16 + i * PLANE, v[2 * i], v[2 * i + 1]);
+  for (int i = 0; i < V / 4; ++i) put16(s + lane * 16 + i * 512, v[2 * i], v[2 * i + 1]);
 }
-template <int V, int PLANE = 512>
+template <int V>
 __device__ __forceinline__ void kept(const char* s, int lane, P2 (&v)[V / 2]) {
 #pragma unroll
-  for (int i = 0; i < V / 4; ++i) get16(s + lane * 16 + i * PLANE, v[2 * i], v[2 * i + 1]);
+  for (int i = 0; i < V / 4; ++i) get16(s + lane * 16 + i * 512, v[2 * i], v[2 * i + 1]);
 }
+
+// A lane's elements of a row of partial weight gradients (whole vectors, see
+// pitch).
+template <int V, bool ODD>
+struct PartRow {
+  __device__ __forceinline__ static void put(float* row, int c, int lane, int C, const P2 (&v)[V / 2]) {
+    if constexpr (ODD) {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i)
+        if (c + 64 * i + 2 * lane < C) *reinterpret_cast<P2*>(row + c + 64 * i + 2 * lane) = v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) put16(row + c + 4 * i, v[2 * i], v[2 * i + 1]);
+    }
+  }
+  __device__ __forceinline__ static void get(const float* row, int c, int lane, int C, P2 (&v)[V / 2]) {
+    if constexpr (ODD) {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i)
+        v[i] = c + 64 * i + 2 * lane < C ? *reinterpret_cast<const P2*>(row + c + 64 * i + 2 * lane) : 0;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) get16(row + c + 4 * i, v[2 * i], v[2 * i + 1]);
+    }
+  }
+};
 
 // Add a b to a thread's share of a weight gradient: in shared memory at s,
 // or, where rows are too long for that, in the group's row of the partial
 // sums (global memory that only this thread touches; such groups are CTAs).
-template <int V>
-__device__ __forceinline__ void add_share(char* s, int lane, float* g, const P2 (&a)[V / 2], const P2 (&b)[V / 2]) {
+template <int V, bool ODD>
+__device__ __forceinline__ void add_share(char* s, float* row, int c, int lane, int C, const P2 (&a)[V / 2],
+                                          const P2 (&b)[V / 2]) {
   P2 d[V / 2];
-  if (g == nullptr) {
+  if (row == nullptr) {
     kept<V>(s, lane, d);
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) d[i] = fma2(a[i], b[i], d[i]);
     keep<V>(s, lane, d);
   } else {
-    kept<V, 16>(reinterpret_cast<const char*>(g), 0, d);
+    PartRow<V, ODD>::get(row, c, lane, C, d);
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) d[i] = fma2(a[i], b[i], d[i]);
-    keep<V, 16>(reinterpret_cast<char*>(g), 0, d);
+    PartRow<V, ODD>::put(row, c, lane, C, d);
   }
 }
 
@@ -327,28 +415,35 @@ struct Any {
   __device__ __forceinline__ float at(int i) const {
     return bf16 ? b4::bf16lo(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
   }
-  // Elements [i, i + V), 1 where there are none (left: elements from i on).
-  // W says what is known of them: nothing (0), or that they are there, on 16
-  // bytes, and fp32 (1) or bf16 (2).  Told apart at run time, both types'
+  // A lane's elements of a block of a weight (as Row has them), 1 where there
+  // is none.  W says what is known of it: nothing (0), or that it is there, on
+  // 16 bytes, and fp32 (1) or bf16 (2).  Told apart at run time, both types'
   // loads, conversions and choices between them are issued every time.
   template <int V, bool ODD, int W>
-  __device__ __forceinline__ void load(int i, int left, P2 (&v)[V / 2]) const {
+  __device__ __forceinline__ void load(int c, int lane, int C, P2 (&v)[V / 2]) const {
     if (W == 0 && p == nullptr) {
 #pragma unroll
       for (int k = 0; k < V / 2; ++k) v[k] = twice(1.0f);
-    } else if (ODD && (W == 0 || left < V)) {
+    } else if constexpr (ODD) {
 #pragma unroll
-      for (int k = 0; k < V / 2; ++k)
-        v[k] = pair(2 * k < left ? at(i + 2 * k) : 0.0f, 2 * k + 1 < left ? at(i + 2 * k + 1) : 0.0f);
+      for (int k = 0; k < V / 2; ++k) {
+        const int e = c + 64 * k + 2 * lane;
+        if (W == 1 && e + 1 < C) {
+          const float2 q = *reinterpret_cast<const float2*>(static_cast<const float*>(p) + e);
+          v[k] = pair(q.x, q.y);
+        } else {
+          v[k] = pair(e < C ? at(e) : 0.0f, W != 1 && e + 1 < C ? at(e + 1) : 0.0f);
+        }
+      }
     } else if (W == 2 || (W == 0 && bf16)) {
 #pragma unroll
       for (int k = 0; k < V / 4; ++k) {
-        const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i + 4 * k);
+        const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + c + 4 * k);
         v[2 * k] = pair(b4::bf16lo(q.x), b4::bf16hi(q.x)), v[2 * k + 1] = pair(b4::bf16lo(q.y), b4::bf16hi(q.y));
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < V / 4; ++k) get16(static_cast<const float*>(p) + i + 4 * k, v[2 * k], v[2 * k + 1]);
+      for (int k = 0; k < V / 4; ++k) get16(static_cast<const float*>(p) + c + 4 * k, v[2 * k], v[2 * k + 1]);
     }
   }
 };
@@ -396,16 +491,23 @@ __device__ __forceinline__ const T* at_row(const void* p, uint32_t t, uint32_t s
   return static_cast<const T*>(p) + uint64_t(t) * stride;
 }
 
+// The channel that a thread of a group has in its first block (ODD: its
+// warp's first channel there).
+template <int V, bool ODD>
+__device__ __forceinline__ int first_channel(int l) {
+  return ODD ? l / 32 * 32 * V : l * V;
+}
+
 // Floats of a row of partial weight gradients: whole vectors.
 __host__ __device__ constexpr int pitch(int C) { return (C + 7) / 8 * 8; }
 
 // Write a CTA's sums of its NG groups' shares to its row (group 0's threads).
 // `first`: where the first item of this thread's warp is in group 0.
-template <int V>
+template <int V, bool ODD>
 __device__ __forceinline__ void sum_shares(const char* first, const Params& p, int NG, int item, float* row) {
   if (threadIdx.x >= p.G) return;
   const int lane = threadIdx.x & 31;
-  for (int c = threadIdx.x * V; c < p.C; c += p.G * V, first += item) {
+  for (int c = first_channel<V, ODD>(threadIdx.x); c < p.C; c += p.G * V, first += item) {
     P2 d[V / 2];
     kept<V>(first, lane, d);
     for (int g = 1; g < NG; ++g) {
@@ -414,7 +516,7 @@ __device__ __forceinline__ void sum_shares(const char* first, const Params& p, i
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) d[j] = add2(d[j], more[j]);
     }
-    keep<V, 16>(reinterpret_cast<char*>(row + c), 0, d);
+    PartRow<V, ODD>::put(row, c, lane, p.C, d);
   }
 }
 

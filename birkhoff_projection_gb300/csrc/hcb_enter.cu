@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
   extern __shared__ __align__(16) char smem[];
   const int G = p.G, NG = blockDim.x / G, group = threadIdx.x / G, l = threadIdx.x % G;
   const int lane = threadIdx.x & 31, warp = l / 32, C = p.C, S = EXACT ? SP : p.S, GV = G * V;
-  const int K = (C + GV - 1) / GV;
+  const int K = (C + GV - 1) / GV, c0 = first_channel<V, ODD>(l);
   char* of_group = smem + group * p.group_bytes;
   char* ring = of_group + warp * p.warp_bytes;
   char* item0 = ring + DEPTH * E::SLOT;
@@ -58,18 +58,19 @@ __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
   uint32_t t = blockIdx.x * NG + group;
 
   uint32_t ta = t;  // the next item to copy
-  int ca = l * V, ka = 0;
+  int ca = c0, ka = 0;
   char* slot_a = ring;
   const TX* xa = at_row<TX>(p.x, ta, p.x_ts);
   auto copy_next = [&] {
+    slot_read<ODD>();
     if (ta < p.T && ca < C) {
 #pragma unroll
       for (int i = 0; i < SP; ++i)
-        if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, xa + i * p.x_ss + ca, C - ca);
+        if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, xa + i * p.x_ss, ca, C);
     }
     copy_commit();
     ca += GV;
-    if (++ka == K) ka = 0, ca = l * V, ta += step, xa = at_row<TX>(p.x, ta, p.x_ts);
+    if (++ka == K) ka = 0, ca = c0, ta += step, xa = at_row<TX>(p.x, ta, p.x_ts);
     slot_a = slot_a == ring + (DEPTH - 1) * E::SLOT ? ring : slot_a + E::SLOT;
   };
   Co co;
@@ -89,15 +90,15 @@ __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
     P2 ss = 0;
     char* item = item0;
 #pragma unroll 1
-    for (int c = l * V, k = 0; k < K; ++k, c += GV, item += E::ITEM) {
-      copy_wait<DEPTH - 1>();
+    for (int c = c0, k = 0; k < K; ++k, c += GV, item += E::ITEM) {
+      slot_ready<DEPTH, ODD>();
       P2 u[H] = {};
       if (c < C) {
 #pragma unroll
         for (int i = 0; i < SP; ++i) {
           if (EXACT || i < S) {
             P2 xv[H];
-            RX::arrived(slot + i * RX::SLOT, lane, x + i * p.x_ss + c, xv);
+            RX::arrived(slot + i * RX::SLOT, lane, x + i * p.x_ss, c, xv);
 #pragma unroll
             for (int j = 0; j < H; ++j) u[j] = fma2(a[i], xv[j], u[j]);
           }
@@ -116,13 +117,13 @@ __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
     TY* h = static_cast<TY*>(p.h) + uint64_t(t) * uint32_t(C);
     item = item0;
 #pragma unroll 1
-    for (int c = l * V; c < C; c += GV, item += E::ITEM) {
+    for (int c = c0; c < C; c += GV, item += E::ITEM) {
       P2 u[H], w[H];
       kept<V>(item, lane, u);
-      p.w.load<V, ODD, W>(c, C - c, w);
+      p.w.load<V, ODD, W>(c, lane, C, w);
 #pragma unroll
       for (int j = 0; j < H; ++j) u[j] = mul2(u[j], mul2(r, w[j]));
-      RY::store(h + c, u, C - c);
+      RY::store(h, c, lane, C, u);
     }
   }
   copy_wait_all();
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
   extern __shared__ __align__(16) char smem[];
   const int G = p.G, NG = blockDim.x / G, group = threadIdx.x / G, l = threadIdx.x % G;
   const int lane = threadIdx.x & 31, warp = l / 32, C = p.C, S = EXACT ? SP : p.S, GV = G * V;
-  const int K = (C + GV - 1) / GV;
+  const int K = (C + GV - 1) / GV, c0 = first_channel<V, ODD>(l);
   const bool direct = !EXACT && p.direct;
   const int ITEM = direct ? E::KW : E::ITEM;
   char* of_group = smem + group * p.group_bytes;
@@ -179,9 +180,10 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
   // items of a token: x and dh for every k, then, if there is one, dres
   const int NI = p.dres ? 2 * K : K;
   uint32_t ta = t;
-  int ca = l * V, ia = 0;
+  int ca = c0, ia = 0;
   char* slot_a = ring;
   auto copy_next = [&] {
+    slot_read<ODD>();
     const bool second = ia >= K;
     if (ta < p.T && ca < C) {
       const TX* x = second ? at_row<TX>(p.dres, ta, p.dres_ts)
@@ -189,15 +191,15 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
       const int64_t ss = second ? p.dres_ss : p.x_ss;
 #pragma unroll
       for (int i = 0; i < SP; ++i)
-        if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, x + i * ss + ca, C - ca);
+        if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, x + i * ss, ca, C);
       if (!second)
-        RY::copy(slot_a + E::DH, lane, at_row<TY>(p.dh, ta, p.dh_ts) + ca, C - ca);
+        RY::copy(slot_a + E::DH, lane, at_row<TY>(p.dh, ta, p.dh_ts), ca, C);
     }
     copy_commit();
     ca += GV;
     ++ia;
-    if (ia == K) ca = l * V;
-    if (ia == NI) ia = 0, ca = l * V, ta += step;
+    if (ia == K) ca = c0;
+    if (ia == NI) ia = 0, ca = c0, ta += step;
     slot_a = slot_a == ring + (DEPTH - 1) * E::SLOT ? ring : slot_a + E::SLOT;
   };
   Co co;
@@ -209,9 +211,9 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
     const P2 z[H] = {};
     char* item = item0;
 #pragma unroll 1
-    for (int c = l * V; c < C; c += GV, item += ITEM) {
+    for (int c = c0; c < C; c += GV, item += ITEM) {
       if (row_dw)
-        keep<V, 16>(reinterpret_cast<char*>(row_dw + c), 0, z);
+        PartRow<V, ODD>::put(row_dw, c, lane, C, z);
       else
         keep<V>(item + E::KW, lane, z);
     }
@@ -229,21 +231,21 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
     P2 sum2[2 * SP] = {};
     char* item = item0;
 #pragma unroll 1
-    for (int c = l * V, k = 0; k < K; ++k, c += GV, item += ITEM) {
+    for (int c = c0, k = 0; k < K; ++k, c += GV, item += ITEM) {
       P2 w[H];
-      if (c < C) p.w.load<V, ODD, W>(c, C - c, w);
-      copy_wait<DEPTH - 1>();
+      if (c < C) p.w.load<V, ODD, W>(c, lane, C, w);
+      slot_ready<DEPTH, ODD>();
       if (c < C) {
         P2 xv[SP][H], g[H], u[H] = {};
 #pragma unroll
         for (int i = 0; i < SP; ++i) {
           if (EXACT || i < S) {
-            RX::arrived(slot + i * RX::SLOT, lane, x + i * p.x_ss + c, xv[i]);
+            RX::arrived(slot + i * RX::SLOT, lane, x + i * p.x_ss, c, xv[i]);
 #pragma unroll
             for (int j = 0; j < H; ++j) u[j] = fma2(a[i], xv[i][j], u[j]);
           }
         }
-        RY::arrived_kept(slot + E::DH, lane, dh + c, g, item + E::KH);
+        RY::arrived_kept(slot + E::DH, lane, dh, c, g, item + E::KH);
 #pragma unroll
         for (int j = 0; j < H; ++j) g[j] = mul2(g[j], w[j]);
 #pragma unroll
@@ -283,16 +285,16 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
     TX* dx = p.dx ? static_cast<TX*>(p.dx) + uint64_t(t) * uint32_t(S * C) : nullptr;
     item = item0;
 #pragma unroll 1
-    for (int c = l * V, k = 0; k < K; ++k, c += GV, item += ITEM) {
-      if (dres) copy_wait<DEPTH - 1>();
+    for (int c = c0, k = 0; k < K; ++k, c += GV, item += ITEM) {
+      if (dres) slot_ready<DEPTH, ODD>();
       if (c < C) {
         P2 u[H], g[H], w[H];
         kept<V>(item, lane, u);
         RY::kept(item + E::KH, lane, g);
-        p.w.load<V, ODD, W>(c, C - c, w);
+        p.w.load<V, ODD, W>(c, lane, C, w);
 #pragma unroll
         for (int j = 0; j < H; ++j) u[j] = mul2(r2, u[j]);
-        if (p.dw) add_share<V>(item + E::KW, lane, row_dw ? row_dw + c : nullptr, g, u);
+        if (p.dw) add_share<V, ODD>(item + E::KW, row_dw, c, lane, C, g, u);
 #pragma unroll
         for (int j = 0; j < H; ++j) u[j] = fma2(mul2(r2, w[j]), g[j], mul2(minus_k, u[j]));
         if (dx) {
@@ -300,10 +302,10 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
           for (int i = 0; i < SP; ++i) {
             if (EXACT || i < S) {
               P2 d[H] = {};
-              if (dres) RX::arrived(slot + i * RX::SLOT, lane, dres + i * p.dres_ss + c, d);
+              if (dres) RX::arrived(slot + i * RX::SLOT, lane, dres + i * p.dres_ss, c, d);
 #pragma unroll
               for (int j = 0; j < H; ++j) d[j] = fma2(a[i], u[j], d[j]);
-              RX::store(dx + i * C + c, d, C - c);
+              RX::store(dx + i * C, c, lane, C, d);
             }
           }
         }
@@ -317,7 +319,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Para
   copy_wait_all();
   if (p.dw && !direct) {
     __syncthreads();
-    sum_shares<V>(smem + warp * p.warp_bytes + DEPTH * E::SLOT + E::KW, p, NG, ITEM,
+    sum_shares<V, ODD>(smem + warp * p.warp_bytes + DEPTH * E::SLOT + E::KW, p, NG, ITEM,
                   p.dw + int64_t(blockIdx.x) * pitch(C));
   }
 }

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
   extern __shared__ __align__(16) char smem[];
   const int G = p.G, NG = blockDim.x / G, group = threadIdx.x / G, l = threadIdx.x % G;
   const int lane = threadIdx.x & 31, warp = l / 32, C = p.C, S = EXACT ? SP : p.S, GV = G * V;
-  const int K = (C + GV - 1) / GV;
+  const int K = (C + GV - 1) / GV, c0 = first_channel<V, ODD>(l);
   char* of_group = smem + group * p.group_bytes;
   char* ring = of_group + warp * p.warp_bytes;
   char* item0 = ring + DEPTH * E::SLOT;
@@ -60,25 +60,26 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
   uint32_t t = blockIdx.x * NG + group;
 
   uint32_t ta = t;
-  int ca = l * V, ia = 0;
+  int ca = c0, ia = 0;
   char* slot_a = ring;
   auto copy_next = [&] {
+    slot_read<ODD>();
     if (ta < p.T && ca < C) {
       if (ia >= K) {
-        const TX* x = at_row<TX>(p.x, ta, p.x_ts) + ca;
+        const TX* x = at_row<TX>(p.x, ta, p.x_ts);
 #pragma unroll
         for (int i = 0; i < SP; ++i)
-          if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, x + i * p.x_ss, C - ca);
+          if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, x + i * p.x_ss, ca, C);
       } else {
-        RY::copy(slot_a + E::Y, lane, at_row<TY>(p.y, ta, p.y_ts) + ca, C - ca);
-        if (gated) RY::copy(slot_a + E::Y + RY::SLOT, lane, at_row<TY>(p.gate, ta, p.gate_ts) + ca, C - ca);
+        RY::copy(slot_a + E::Y, lane, at_row<TY>(p.y, ta, p.y_ts), ca, C);
+        if (gated) RY::copy(slot_a + E::Y + RY::SLOT, lane, at_row<TY>(p.gate, ta, p.gate_ts), ca, C);
       }
     }
     copy_commit();
     ca += GV;
     ++ia;
-    if (ia == K) ca = l * V;
-    if (ia == 2 * K) ia = 0, ca = l * V, ta += step;
+    if (ia == K) ca = c0;
+    if (ia == 2 * K) ia = 0, ca = c0, ta += step;
     slot_a = slot_a == ring + (DEPTH - 1) * E::SLOT ? ring : slot_a + E::SLOT;
   };
   Co co;
@@ -98,13 +99,13 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
     P2 ss = 0;
     char* item = item0;
 #pragma unroll 1
-    for (int c = l * V, k = 0; k < K; ++k, c += GV, item += E::ITEM) {
+    for (int c = c0, k = 0; k < K; ++k, c += GV, item += E::ITEM) {
       P2 w[H];
-      if (c < C) p.w.load<V, ODD, W>(c, C - c, w);
-      copy_wait<DEPTH - 1>();
+      if (c < C) p.w.load<V, ODD, W>(c, lane, C, w);
+      slot_ready<DEPTH, ODD>();
       if (c < C) {
         P2 v[H];
-        RY::arrived(slot + E::Y, lane, y + c, v);
+        RY::arrived(slot + E::Y, lane, y, c, v);
 #pragma unroll
         for (int j = 0; j < H; ++j) {
           ss = fma2(v[j], v[j], ss);
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
         }
         if (gated) {
           P2 g[H];
-          RY::arrived(slot + E::Y + RY::SLOT, lane, gate + c, g);
+          RY::arrived(slot + E::Y + RY::SLOT, lane, gate, c, g);
           gates<V, false>(p.act, g, w);
 #pragma unroll
           for (int j = 0; j < H; ++j) v[j] = mul2(v[j], g[j]);
@@ -137,15 +138,15 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
     ss = 0;
     item = item0;
 #pragma unroll 1
-    for (int c = l * V, k = 0; k < K; ++k, c += GV, item += E::ITEM) {
-      copy_wait<DEPTH - 1>();
+    for (int c = c0, k = 0; k < K; ++k, c += GV, item += E::ITEM) {
+      slot_ready<DEPTH, ODD>();
       if (c < C) {
         P2 v[H], xv[SP][H], u[H] = {};
         kept<V>(item, lane, v);
 #pragma unroll
         for (int i = 0; i < SP; ++i) {
           if (EXACT || i < S) {
-            RX::arrived(slot + i * RX::SLOT, lane, x + i * p.x_ss + c, xv[i]);
+            RX::arrived(slot + i * RX::SLOT, lane, x + i * p.x_ss, c, xv[i]);
           } else {
 #pragma unroll
             for (int j = 0; j < H; ++j) xv[i][j] = 0;
@@ -171,11 +172,11 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
               for (int j = 0; j < H; ++j) o[j] = fma2(b[i], v[j], xv[i][j]);
             }
             if (p.h) {
-              RX::store_rounded(out + i * C + c, o, C - c);
+              RX::store_rounded(out + i * C, c, lane, C, o);
 #pragma unroll
               for (int j = 0; j < H; ++j) u[j] = fma2(a[i], o[j], u[j]);
             } else {
-              RX::store(out + i * C + c, o, C - c);
+              RX::store(out + i * C, c, lane, C, o);
             }
           }
         }
@@ -196,13 +197,13 @@ __global__ void __launch_bounds__(SP == 8 ? 256 : kMaxGroup, 1) leave_kernel(con
       TY* h = static_cast<TY*>(p.h) + uint64_t(t) * uint32_t(C);
       item = item0;
 #pragma unroll 1
-      for (int c = l * V; c < C; c += GV, item += E::ITEM) {
+      for (int c = c0; c < C; c += GV, item += E::ITEM) {
         P2 u[H], w[H];
         kept<V>(item, lane, u);
-        p.wn.load<V, ODD, W>(c, C - c, w);
+        p.wn.load<V, ODD, W>(c, lane, C, w);
 #pragma unroll
         for (int j = 0; j < H; ++j) u[j] = mul2(u[j], mul2(r, w[j]));
-        RY::store(h + c, u, C - c);
+        RY::store(h, c, lane, C, u);
       }
     }
   }

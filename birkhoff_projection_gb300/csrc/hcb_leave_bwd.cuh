@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
   extern __shared__ __align__(16) char smem[];
   const int G = p.G, NG = blockDim.x / G, group = threadIdx.x / G, l = threadIdx.x % G;
   const int lane = threadIdx.x & 31, warp = l / 32, C = p.C, S = EXACT ? SP : p.S, GV = G * V;
-  const int K = (C + GV - 1) / GV;
+  const int K = (C + GV - 1) / GV, c0 = first_channel<V, ODD>(l);
   const bool direct = !EXACT && p.direct;
   const bool mix = EXACT ? SP > 1 : p.P.p != nullptr, gated = GATE == 2 ? p.gate != nullptr : GATE != 0;
   const int SLOT = E::slot(mix, gated), ITEM = E::item(gated, direct), KB = E::kb(direct);
@@ -88,36 +88,37 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
 
   const int NI = NEXT ? 2 * K : K;
   uint32_t ta = t;
-  int ca = l * V, ia = 0;
+  int ca = c0, ia = 0;
   char* slot_a = ring;
   auto copy_next = [&] {
+    slot_read<ODD>();
     if (ta < p.T && ca < C) {
       if (NEXT && ia < K) {
-        const TX* o = at_row<TX>(p.out_in, ta, p.out_ts) + ca;
+        const TX* o = at_row<TX>(p.out_in, ta, p.out_ts);
 #pragma unroll
         for (int i = 0; i < SP; ++i)
-          if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, o + i * p.out_ss, C - ca);
-        RY::copy(slot_a + E::Y, lane, at_row<TY>(p.dh, ta, p.dh_ts) + ca, C - ca);
+          if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, o + i * p.out_ss, ca, C);
+        RY::copy(slot_a + E::Y, lane, at_row<TY>(p.dh, ta, p.dh_ts), ca, C);
       } else {
-        const TX* d = at_row<TX>(p.dout, ta, p.dout_ts) + ca;
+        const TX* d = at_row<TX>(p.dout, ta, p.dout_ts);
 #pragma unroll
         for (int i = 0; i < SP; ++i)
-          if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, d + i * p.dout_ss, C - ca);
-        RY::copy(slot_a + E::Y, lane, at_row<TY>(p.y, ta, p.y_ts) + ca, C - ca);
-        if (gated) RY::copy(slot_a + E::GATE, lane, at_row<TY>(p.gate, ta, p.gate_ts) + ca, C - ca);
+          if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, d + i * p.dout_ss, ca, C);
+        RY::copy(slot_a + E::Y, lane, at_row<TY>(p.y, ta, p.y_ts), ca, C);
+        if (gated) RY::copy(slot_a + E::GATE, lane, at_row<TY>(p.gate, ta, p.gate_ts), ca, C);
         if (mix) {
-          const TX* x = at_row<TX>(p.x, ta, p.x_ts) + ca;
+          const TX* x = at_row<TX>(p.x, ta, p.x_ts);
 #pragma unroll
           for (int i = 0; i < SP; ++i)
-            if (EXACT || i < S) RX::copy(slot_a + E::X + i * RX::SLOT, lane, x + i * p.x_ss, C - ca);
+            if (EXACT || i < S) RX::copy(slot_a + E::X + i * RX::SLOT, lane, x + i * p.x_ss, ca, C);
         }
       }
     }
     copy_commit();
     ca += GV;
     ++ia;
-    if (NEXT && ia == K) ca = l * V;
-    if (ia == NI) ia = 0, ca = l * V, ta += step;
+    if (NEXT && ia == K) ca = c0;
+    if (ia == NI) ia = 0, ca = c0, ta += step;
     if constexpr (DEPTH > 1) slot_a = slot_a == ring + (DEPTH - 1) * SLOT ? ring : slot_a + SLOT;
   };
   Co co;
@@ -129,10 +130,10 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
     const P2 z[H] = {};
     char* item = item0;
 #pragma unroll 1
-    for (int c = l * V; c < C; c += GV, item += ITEM) {
+    for (int c = c0; c < C; c += GV, item += ITEM) {
       if (direct) {
-        if (row_dw) keep<V, 16>(reinterpret_cast<char*>(row_dw + c), 0, z);
-        if (NEXT && row_dwn) keep<V, 16>(reinterpret_cast<char*>(row_dwn + c), 0, z);
+        if (row_dw) PartRow<V, ODD>::put(row_dw, c, lane, C, z);
+        if (NEXT && row_dwn) PartRow<V, ODD>::put(row_dwn, c, lane, C, z);
       } else {
         keep<V>(item + E::KW, lane, z);
         if constexpr (NEXT) keep<V>(item + E::KN, lane, z);
@@ -153,24 +154,24 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
       Co::read(co_s, Co::NB, a);
       char* item = item0;
 #pragma unroll 1
-      for (int c = l * V, k = 0; k < K; ++k, c += GV, item += ITEM) {
+      for (int c = c0, k = 0; k < K; ++k, c += GV, item += ITEM) {
         P2 w[H];
-        if (c < C) p.wn.load<V, ODD, W>(c, C - c, w);
-        copy_wait<DEPTH - 1>();
+        if (c < C) p.wn.load<V, ODD, W>(c, lane, C, w);
+        slot_ready<DEPTH, ODD>();
         if (c < C) {
           P2 xv[SP][H], g[H], u[H] = {};
 #pragma unroll
           for (int i = 0; i < SP; ++i) {
             if (EXACT || i < S) {
-              RX::arrived(slot + i * RX::SLOT, lane, o + i * p.out_ss + c, xv[i]);
+              RX::arrived(slot + i * RX::SLOT, lane, o + i * p.out_ss, c, xv[i]);
 #pragma unroll
               for (int j = 0; j < H; ++j) u[j] = fma2(a[i], xv[i][j], u[j]);
             }
           }
           if (direct)
-            RY::arrived(slot + E::Y, lane, dh + c, g);
+            RY::arrived(slot + E::Y, lane, dh, c, g);
           else
-            RY::arrived_kept(slot + E::Y, lane, dh + c, g, item + E::KH);
+            RY::arrived_kept(slot + E::Y, lane, dh, c, g, item + E::KH);
 #pragma unroll
           for (int j = 0; j < H; ++j) g[j] = mul2(g[j], w[j]);
 #pragma unroll
@@ -215,24 +216,24 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
     TX* dx = p.dx ? static_cast<TX*>(p.dx) + uint64_t(t) * uint32_t(S * C) : nullptr;
     char* item = item0;
 #pragma unroll 1
-    for (int c = l * V, k = 0; k < K; ++k, c += GV, item += ITEM) {
+    for (int c = c0, k = 0; k < K; ++k, c += GV, item += ITEM) {
       P2 du[H];
       if (NEXT && c < C) {
         P2 h[H], wn[H];
         const P2 r2 = twice(r_next), minus_k = twice(-k_next);
         kept<V>(item, lane, du);
         if (direct)
-          RY::load(at_row<TY>(p.dh, t, p.dh_ts) + c, h, C - c);
+          RY::load(at_row<TY>(p.dh, t, p.dh_ts), c, lane, C, h);
         else
           RY::kept(item + E::KH, lane, h);
-        p.wn.load<V, ODD, W>(c, C - c, wn);
+        p.wn.load<V, ODD, W>(c, lane, C, wn);
 #pragma unroll
         for (int j = 0; j < H; ++j) du[j] = mul2(r2, du[j]);
-        if (p.dwn) add_share<V>(item + E::KN, lane, row_dwn ? row_dwn + c : nullptr, h, du);
+        if (p.dwn) add_share<V, ODD>(item + E::KN, row_dwn, c, lane, C, h, du);
 #pragma unroll
         for (int j = 0; j < H; ++j) du[j] = fma2(mul2(r2, wn[j]), h[j], mul2(minus_k, du[j]));
       }
-      copy_wait<DEPTH - 1>();
+      slot_ready<DEPTH, ODD>();
       if (c >= C) {
         copy_next();
         if constexpr (DEPTH > 1) slot = slot == ring + (DEPTH - 1) * SLOT ? ring : slot + SLOT;
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
 #pragma unroll
       for (int i = 0; i < SP; ++i) {
         if (EXACT || i < S) {
-          RX::arrived(slot + i * RX::SLOT, lane, dout + i * p.dout_ss + c, D[i]);
+          RX::arrived(slot + i * RX::SLOT, lane, dout + i * p.dout_ss, c, D[i]);
         } else {
 #pragma unroll
           for (int j = 0; j < H; ++j) D[i][j] = 0;
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
         for (int q = 0; q < SP; ++q) {
           if (EXACT || q < S) {
             P2 xv[H];
-            RX::arrived(slot + E::X + q * RX::SLOT, lane, x + q * p.x_ss + c, xv);
+            RX::arrived(slot + E::X + q * RX::SLOT, lane, x + q * p.x_ss, c, xv);
 #pragma unroll
             for (int i = 0; i < SP; ++i)
 #pragma unroll
@@ -279,10 +280,10 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
         }
       }
       if (direct)
-        RY::arrived(slot + E::Y, lane, y + c, e);
+        RY::arrived(slot + E::Y, lane, y, c, e);
       else
-        RY::arrived_kept(slot + E::Y, lane, y + c, e, item + E::KY);
-      if (gated) RY::arrived(slot + E::GATE, lane, gate + c, g);
+        RY::arrived_kept(slot + E::Y, lane, y, c, e, item + E::KY);
+      if (gated) RY::arrived(slot + E::GATE, lane, gate, c, g);
       copy_next();
       if constexpr (DEPTH > 1) slot = slot == ring + (DEPTH - 1) * SLOT ? ring : slot + SLOT;
       if (dx) {
@@ -298,9 +299,9 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
 #pragma unroll
                 for (int i = 1; i < SP; ++i) d[j] = fma2(P[i], D[i][j], d[j]);
               }
-              RX::store(dx + q * C + c, d, C - c);
+              RX::store(dx + q * C, c, lane, C, d);
             } else {
-              RX::store(dx + q * C + c, D[q], C - c);
+              RX::store(dx + q * C, c, lane, C, D[q]);
             }
           }
         }
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
       }
       {
         P2 w[H];
-        p.w.load<V, ODD, W>(c, C - c, w);
+        p.w.load<V, ODD, W>(c, lane, C, w);
 #pragma unroll
         for (int j = 0; j < H; ++j) e[j] = mul2(e[j], w[j]);
       }
@@ -369,10 +370,10 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
     TY* dgate = gated && p.dgate ? static_cast<TY*>(p.dgate) + uint64_t(t) * uint32_t(C) : nullptr;
     item = item0;
 #pragma unroll 1
-    for (int c = l * V; c < C; c += GV, item += ITEM) {
+    for (int c = c0; c < C; c += GV, item += ITEM) {
       P2 yv[H], w[H], d[H];
       if (direct)
-        RY::load(y + c, yv, C - c);
+        RY::load(y, c, lane, C, yv);
       else
         RY::kept(item + E::KY, lane, yv);
       if (dgate) {
@@ -380,17 +381,17 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
         kept<V>(item + KB, lane, g);
 #pragma unroll
         for (int j = 0; j < H; ++j) g[j] = mul2(g[j], sr2);
-        RY::store(dgate + c, g, C - c);
+        RY::store(dgate, c, lane, C, g);
       }
-      p.w.load<V, ODD, W>(c, C - c, w);
+      p.w.load<V, ODD, W>(c, lane, C, w);
       kept<V>(item, lane, d);
 #pragma unroll
       for (int j = 0; j < H; ++j) d[j] = mul2(d[j], sr2);
-      if (p.dw) add_share<V>(item + E::KW, lane, row_dw ? row_dw + c : nullptr, d, yv);
+      if (p.dw) add_share<V, ODD>(item + E::KW, row_dw, c, lane, C, d, yv);
       if (dy) {
 #pragma unroll
         for (int j = 0; j < H; ++j) d[j] = fma2(d[j], w[j], mul2(minus_k, yv[j]));
-        RY::store(dy + c, d, C - c);
+        RY::store(dy, c, lane, C, d);
       }
     }
   }
@@ -399,8 +400,8 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
     __syncthreads();
     const int64_t row = int64_t(blockIdx.x) * pitch(C);
     const char* first = smem + warp * p.warp_bytes + DEPTH * SLOT;
-    if (p.dw) sum_shares<V>(first + E::KW, p, NG, ITEM, p.dw + row);
-    if (NEXT && p.dwn) sum_shares<V>(first + E::KN, p, NG, ITEM, p.dwn + row);
+    if (p.dw) sum_shares<V, ODD>(first + E::KW, p, NG, ITEM, p.dw + row);
+    if (NEXT && p.dwn) sum_shares<V, ODD>(first + E::KN, p, NG, ITEM, p.dwn + row);
   }
 }
 
