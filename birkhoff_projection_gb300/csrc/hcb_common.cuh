@@ -112,7 +112,8 @@ __device__ __forceinline__ void put16(void* p, P2 a, P2 b) {
 // ---------------------------------------------------------------------------
 // A lane's V elements of a block of a row, and their way through shared
 // memory.  `row` is the row's first element and c the lane's first channel
-// (ODD: the block's), below C.
+// (ODD: the block's).  From C on there are zeros, and nothing is written, so
+// that the lanes and blocks behind a row's end need no branches of their own.
 //
 // ODD rows need not lie on 16-byte boundaries (any alignment of the element
 // type) and end with C wherever that is.  They are copied in 4-byte words.
@@ -124,11 +125,11 @@ __device__ __forceinline__ void put16(void* p, P2 a, P2 b) {
 __device__ __forceinline__ void copy4(uint32_t d, const void* p) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(p) : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t d, const void* p) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(p) : "memory");
+__device__ __forceinline__ void copy8(uint32_t d, const void* p, int n = 8) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(p), "r"(n) : "memory");
 }
-__device__ __forceinline__ void copy16(uint32_t d, const void* p) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(p) : "memory");
+__device__ __forceinline__ void copy16(uint32_t d, const void* p, int n = 16) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(p), "r"(n) : "memory");
 }
 // n of 4 bytes, the rest zero; p is not read if n <= 0 but has to be valid
 __device__ __forceinline__ void copy4_of(uint32_t d, const void* p, const void* valid, int n) {
@@ -158,13 +159,15 @@ struct Row {
   __device__ __forceinline__ static void copy(char* s, int lane, const T* row, int c, int C) {
     if constexpr (!ODD) {
       const uint32_t d = b4::smem_addr(s + lane * BYTES);
+      const T* p = row + min(c, C - V);
       if constexpr (BYTES == 16)
-        copy16(d, row + c);
+        copy16(d, p, c < C ? 16 : 0);
       else
-        copy8(d, row + c);
+        copy8(d, p, c < C ? 8 : 0);
     } else if constexpr (SPLIT) {
       const int before = straddles(row, c);
       const char* block = reinterpret_cast<const char*>(row + c) - before;
+      const char* valid = reinterpret_cast<const char*>(row) - straddles(row, 0);
       const char* p = block + 4 * lane;
       const uint32_t d = b4::smem_addr(s + 4 * lane);
       if (c + 32 * V + 2 <= C) {  // all of its words lie within the row
@@ -174,9 +177,9 @@ struct Row {
       } else {
         const int end = 2 * (C - c) + before - 4 * lane;  // bytes from p to the row's end
 #pragma unroll
-        for (int i = 0; i < H; ++i) copy4_of(d + 128 * i, p + 128 * i, block, end - 128 * i);
+        for (int i = 0; i < H; ++i) copy4_of(d + 128 * i, p + 128 * i, valid, end - 128 * i);
         if (before && lane == 31)
-          copy4_of(d + 128 * (H - 1) + 4, p + 128 * (H - 1) + 4, block, end - 128 * (H - 1) - 4);
+          copy4_of(d + 128 * (H - 1) + 4, p + 128 * (H - 1) + 4, valid, end - 128 * (H - 1) - 4);
       }
     } else {
       const T* p = row + c + 2 * lane;
@@ -226,7 +229,7 @@ struct Row {
       }
     } else {
       uint32_t w[BYTES / 4];
-      words(reinterpret_cast<const char*>(row + c), w);
+      words(reinterpret_cast<const char*>(row + min(c, C - V)), w);
       unpack(w, v);
     }
   }
@@ -298,6 +301,7 @@ struct Row {
   }
   __device__ __forceinline__ static void put(T* row, int c, int lane, int C, const uint32_t (&w)[BYTES / 4]) {
     if constexpr (!ODD) {
+      if (c >= C) return;
       if constexpr (BYTES == 16)
         *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
       else
@@ -334,9 +338,14 @@ struct Row {
   }
 };
 
-// The oldest of DEPTH copies has arrived; a slot has been read and may be
+// All of the thread's copies, or the oldest of DEPTH, have arrived; a slot has been read and may be
 // copied to again.  A lane of an ODD kernel reads a word of its neighbour's,
 // so there the warp waits for each other (all of its branches are the warp's).
+template <bool ODD>
+__device__ __forceinline__ void slots_ready() {
+  copy_wait_all();
+  if constexpr (ODD) __syncwarp();
+}
 template <int DEPTH, bool ODD>
 __device__ __forceinline__ void slot_ready() {
   copy_wait<DEPTH - 1>();
@@ -370,7 +379,7 @@ struct PartRow {
 #pragma unroll
       for (int i = 0; i < V / 2; ++i)
         if (c + 64 * i + 2 * lane < C) *reinterpret_cast<P2*>(row + c + 64 * i + 2 * lane) = v[i];
-    } else {
+    } else if (c < C) {
 #pragma unroll
       for (int i = 0; i < V / 4; ++i) put16(row + c + 4 * i, v[2 * i], v[2 * i + 1]);
     }
@@ -382,7 +391,7 @@ struct PartRow {
         v[i] = c + 64 * i + 2 * lane < C ? *reinterpret_cast<const P2*>(row + c + 64 * i + 2 * lane) : 0;
     } else {
 #pragma unroll
-      for (int i = 0; i < V / 4; ++i) get16(row + c + 4 * i, v[2 * i], v[2 * i + 1]);
+      for (int i = 0; i < V / 4; ++i) get16(row + min(c, C - V) + 4 * i, v[2 * i], v[2 * i + 1]);
     }
   }
 };
@@ -415,8 +424,8 @@ struct Any {
   __device__ __forceinline__ float at(int i) const {
     return bf16 ? b4::bf16lo(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
   }
-  // A lane's elements of a block of a weight (as Row has them), 1 where there
-  // is none.  W says what is known of it: nothing (0), or that it is there, on
+  // A lane's elements of a block of a weight (as Row has them; from C on any
+  // of its values), 1 where there is none.  W says what is known of it: nothing (0), or that it is there, on
   // 16 bytes, and fp32 (1) or bf16 (2).  Told apart at run time, both types'
   // loads, conversions and choices between them are issued every time.
   template <int V, bool ODD, int W>
@@ -438,12 +447,12 @@ struct Any {
     } else if (W == 2 || (W == 0 && bf16)) {
 #pragma unroll
       for (int k = 0; k < V / 4; ++k) {
-        const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + c + 4 * k);
+        const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + min(c, C - V) + 4 * k);
         v[2 * k] = pair(b4::bf16lo(q.x), b4::bf16hi(q.x)), v[2 * k + 1] = pair(b4::bf16lo(q.y), b4::bf16hi(q.y));
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < V / 4; ++k) get16(static_cast<const float*>(p) + c + 4 * k, v[2 * k], v[2 * k + 1]);
+      for (int k = 0; k < V / 4; ++k) get16(static_cast<const float*>(p) + min(c, C - V) + 4 * k, v[2 * k], v[2 * k + 1]);
     }
   }
 };

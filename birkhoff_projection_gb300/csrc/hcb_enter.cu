@@ -8,6 +8,9 @@
 #ifndef HCB_ENTER_BWD_DEPTH
 #define HCB_ENTER_BWD_DEPTH 2
 #endif
+#ifndef HCB_ENTER_BWD_MINB
+#define HCB_ENTER_BWD_MINB 2
+#endif
 #ifndef HCB_ENTER_PER
 #define HCB_ENTER_PER 2
 #endif
@@ -150,7 +153,7 @@ struct EnterBackward {
 };
 
 template <int SP, bool EXACT, class TX, class TY, int V, bool ODD, int W>
-__global__ void __launch_bounds__(kMaxGroup, 1) enter_backward_kernel(const Params p) {
+__global__ void __launch_bounds__(256, SP == 8 ? 1 : HCB_ENTER_BWD_MINB) enter_backward_kernel(const Params p) {
   using E = EnterBackward<SP, TX, TY, V, ODD>;
   using RX = typename E::RX;
   using RY = typename E::RY;
@@ -348,7 +351,7 @@ struct Backward {
   cudaError_t operator()() const {
     Params q = p;
     const Shape sh =
-        plan(q, shape_of(p.T, p.C, V, HCB_ENTER_BWD_PER, kMaxGroup), V, EnterBackward<SP, TX, TY, V, ODD>::need);
+        plan(q, shape_of(p.T, p.C, V, HCB_ENTER_BWD_PER, 256), V, EnterBackward<SP, TX, TY, V, ODD>::need);
     const int most = p.dw ? kMaxRows : 1 << 30;
     const int w = EXACT && !q.direct ? Weights::kind(p.w) : 0;
     if (w == 1) return launch<enter_backward_kernel<SP, EXACT, TX, TY, V, ODD, EXACT ? 1 : 0>>(q, sh, most, rows, s);

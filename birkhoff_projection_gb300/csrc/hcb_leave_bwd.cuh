@@ -5,14 +5,14 @@
 
 #include "hcb_common.cuh"
 
-#ifndef HCB_LEAVE_BWD_DEPTH
-#define HCB_LEAVE_BWD_DEPTH 1
+#ifndef HCB_LEAVE_BWD_PER
+#define HCB_LEAVE_BWD_PER 2
 #endif
 #ifndef HCB_LEAVE_BWD_MINB1
 #define HCB_LEAVE_BWD_MINB1 3
 #endif
-#ifndef HCB_LEAVE_BWD_PER
-#define HCB_LEAVE_BWD_PER 2
+#ifndef HCB_LEAVE_BWD_WHOLE
+#define HCB_LEAVE_BWD_WHOLE 2
 #endif
 
 namespace hcb {
@@ -37,7 +37,6 @@ struct LeaveBackward {
   static constexpr bool PAIRS = SP <= 2 || (SP == 4 && V == 4);
   using Sum = GroupSum<R>;
   using SumNext = GroupSum<2 * SP>;
-  static constexpr int DEPTH = HCB_LEAVE_BWD_DEPTH;
   // CTAs that the registers have to leave room for on an SM
   static constexpr int minb(int gate) { return SP == 1 && gate == 0 ? HCB_LEAVE_BWD_MINB1 : SP <= 4 ? 2 : 1; }
   // a slot: dout, y, gate and x; or the stored result, and dh where y would be
@@ -61,17 +60,22 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
   using RY = typename E::RY;
   using Co = typename E::Co;
   using Sum = typename E::Sum;
-  constexpr int R = E::R, DEPTH = E::DEPTH, H = V / 2;
+  // WHOLE, as in leave_kernel: a slot to every item, each copied to again as
+  // soon as it is read.  For more streams the slots would leave room for fewer
+  // threads: there is one, for the next item.
+  constexpr bool WHOLE = EXACT && SP <= HCB_LEAVE_BWD_WHOLE;
+  constexpr int R = E::R, H = V / 2;
   extern __shared__ __align__(16) char smem[];
   const int G = p.G, NG = blockDim.x / G, group = threadIdx.x / G, l = threadIdx.x % G;
   const int lane = threadIdx.x & 31, warp = l / 32, C = p.C, S = EXACT ? SP : p.S, GV = G * V;
-  const int K = (C + GV - 1) / GV, c0 = first_channel<V, ODD>(l);
+  const int K = (C + GV - 1) / GV, c0 = first_channel<V, ODD>(l), c1 = c0 + K * GV;
   const bool direct = !EXACT && p.direct;
   const bool mix = EXACT ? SP > 1 : p.P.p != nullptr, gated = GATE == 2 ? p.gate != nullptr : GATE != 0;
   const int SLOT = E::slot(mix, gated), ITEM = E::item(gated, direct), KB = E::kb(direct);
+  const int NEXT_SLOT = WHOLE ? SLOT : 0;
   char* of_group = smem + group * p.group_bytes;
   char* ring = of_group + warp * p.warp_bytes;
-  char* item0 = ring + DEPTH * SLOT;
+  char* item0 = ring + (WHOLE ? K : 1) * SLOT;
   float* co_all = reinterpret_cast<float*>(of_group + G / 32 * p.warp_bytes);
   float* co_s = co_all + warp * Co::FLOATS;
   float* red = co_all + G / 32 * Co::FLOATS;
@@ -86,51 +90,37 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
   const uint32_t step = gridDim.x * NG;
   uint32_t t = blockIdx.x * NG + group;
 
-  const int NI = NEXT ? 2 * K : K;
-  uint32_t ta = t;
-  int ca = c0, ia = 0;
-  char* slot_a = ring;
-  auto copy_next = [&] {
-    slot_read<ODD>();
-    if (ta < p.T && ca < C) {
-      if (NEXT && ia < K) {
-        const TX* o = at_row<TX>(p.out_in, ta, p.out_ts);
+  // The two kinds of items: `first`, NEXT's stored result and dh, and the
+  // rest.  (One copy in the code for both: more would cost registers.)
+  auto copy = [&](bool first, uint32_t t, int c, char* slot) {
+    first = NEXT && first;
+    const TX* d = first ? at_row<TX>(p.out_in, t, p.out_ts) : at_row<TX>(p.dout, t, p.dout_ts);
+    const uint32_t ss = first ? p.out_ss : p.dout_ss;
 #pragma unroll
-        for (int i = 0; i < SP; ++i)
-          if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, o + i * p.out_ss, ca, C);
-        RY::copy(slot_a + E::Y, lane, at_row<TY>(p.dh, ta, p.dh_ts), ca, C);
-      } else {
-        const TX* d = at_row<TX>(p.dout, ta, p.dout_ts);
+    for (int i = 0; i < SP; ++i)
+      if (EXACT || i < S) RX::copy(slot + i * RX::SLOT, lane, d + i * ss, c, C);
+    RY::copy(slot + E::Y, lane, first ? at_row<TY>(p.dh, t, p.dh_ts) : at_row<TY>(p.y, t, p.y_ts), c, C);
+    if (first) return;
+    if (gated) RY::copy(slot + E::GATE, lane, at_row<TY>(p.gate, t, p.gate_ts), c, C);
+    if (mix) {
+      const TX* x = at_row<TX>(p.x, t, p.x_ts);
 #pragma unroll
-        for (int i = 0; i < SP; ++i)
-          if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, d + i * p.dout_ss, ca, C);
-        RY::copy(slot_a + E::Y, lane, at_row<TY>(p.y, ta, p.y_ts), ca, C);
-        if (gated) RY::copy(slot_a + E::GATE, lane, at_row<TY>(p.gate, ta, p.gate_ts), ca, C);
-        if (mix) {
-          const TX* x = at_row<TX>(p.x, ta, p.x_ts);
-#pragma unroll
-          for (int i = 0; i < SP; ++i)
-            if (EXACT || i < S) RX::copy(slot_a + E::X + i * RX::SLOT, lane, x + i * p.x_ss, ca, C);
-        }
-      }
+      for (int i = 0; i < SP; ++i)
+        if (EXACT || i < S) RX::copy(slot + E::X + i * RX::SLOT, lane, x + i * p.x_ss, c, C);
     }
-    copy_commit();
-    ca += GV;
-    ++ia;
-    if (NEXT && ia == K) ca = c0;
-    if (ia == NI) ia = 0, ca = c0, ta += step;
-    if constexpr (DEPTH > 1) slot_a = slot_a == ring + (DEPTH - 1) * SLOT ? ring : slot_a + SLOT;
   };
   Co co;
   co.init(p, lane);
-  if (t < p.T) co.fetch(t);
-#pragma unroll
-  for (int d = 0; d < DEPTH; ++d) copy_next();
+  if (t < p.T) {
+    co.fetch(t);
+    char* slot = ring;
+    for (int c = c0; c < (WHOLE ? c1 : c0 + 1); c += GV, slot += NEXT_SLOT) copy(true, t, c, slot);
+  }
   {
     const P2 z[H] = {};
     char* item = item0;
 #pragma unroll 1
-    for (int c = c0; c < C; c += GV, item += ITEM) {
+    for (int c = c0; c < c1; c += GV, item += ITEM) {
       if (direct) {
         if (row_dw) PartRow<V, ODD>::put(row_dw, c, lane, C, z);
         if (NEXT && row_dwn) PartRow<V, ODD>::put(row_dwn, c, lane, C, z);
@@ -141,53 +131,52 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
     }
   }
 
-  const char* slot = ring;
 #pragma unroll 1
   for (; t < p.T; t += step) {
     co.spread(co_s, lane);
-    if (t + step < p.T) co.fetch(t + step);
+    const bool more = t + step < p.T;
+    if (more) co.fetch(t + step);
     float r_next = 0.0f, k_next = 0.0f;
     if constexpr (NEXT) {
       const TX* o = at_row<TX>(p.out_in, t, p.out_ts);
       const TY* dh = at_row<TY>(p.dh, t, p.dh_ts);
       P2 a[SP], sum2[2 * SP] = {};
       Co::read(co_s, Co::NB, a);
-      char* item = item0;
+      char *item = item0, *slot = ring;
+      if (WHOLE) slots_ready<ODD>();
 #pragma unroll 1
-      for (int c = c0, k = 0; k < K; ++k, c += GV, item += ITEM) {
-        P2 w[H];
-        if (c < C) p.wn.load<V, ODD, W>(c, lane, C, w);
-        slot_ready<DEPTH, ODD>();
-        if (c < C) {
-          P2 xv[SP][H], g[H], u[H] = {};
+      for (int c = c0; c < c1; c += GV, item += ITEM, slot += NEXT_SLOT) {
+        P2 xv[SP][H], g[H], w[H], u[H] = {};
+        p.wn.load<V, ODD, W>(c, lane, C, w);
+        if (!WHOLE) slots_ready<ODD>();
 #pragma unroll
-          for (int i = 0; i < SP; ++i) {
-            if (EXACT || i < S) {
-              RX::arrived(slot + i * RX::SLOT, lane, o + i * p.out_ss, c, xv[i]);
+        for (int i = 0; i < SP; ++i) {
+          if (EXACT || i < S) {
+            RX::arrived(slot + i * RX::SLOT, lane, o + i * p.out_ss, c, xv[i]);
 #pragma unroll
-              for (int j = 0; j < H; ++j) u[j] = fma2(a[i], xv[i][j], u[j]);
-            }
+            for (int j = 0; j < H; ++j) u[j] = fma2(a[i], xv[i][j], u[j]);
           }
-          if (direct)
-            RY::arrived(slot + E::Y, lane, dh, c, g);
-          else
-            RY::arrived_kept(slot + E::Y, lane, dh, c, g, item + E::KH);
-#pragma unroll
-          for (int j = 0; j < H; ++j) g[j] = mul2(g[j], w[j]);
-#pragma unroll
-          for (int i = 0; i < SP; ++i) {
-            if (EXACT || i < S) {
-#pragma unroll
-              for (int j = 0; j < H; ++j) {
-                sum2[i] = fma2(g[j], xv[i][j], sum2[i]);
-                sum2[SP + i] = fma2(u[j], xv[i][j], sum2[SP + i]);
-              }
-            }
-          }
-          keep<V>(item, lane, u);
         }
-        copy_next();
-        if constexpr (DEPTH > 1) slot = slot == ring + (DEPTH - 1) * SLOT ? ring : slot + SLOT;
+        if (direct)
+          RY::arrived(slot + E::Y, lane, dh, c, g);
+        else
+          RY::arrived_kept(slot + E::Y, lane, dh, c, g, item + E::KH);
+        slot_read<ODD>();
+        const bool same = !WHOLE && c + GV < c1;
+        copy(same, t, WHOLE ? c : same ? c + GV : c0, slot);
+#pragma unroll
+        for (int j = 0; j < H; ++j) g[j] = mul2(g[j], w[j]);
+#pragma unroll
+        for (int i = 0; i < SP; ++i) {
+          if (EXACT || i < S) {
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+              sum2[i] = fma2(g[j], xv[i][j], sum2[i]);
+              sum2[SP + i] = fma2(u[j], xv[i][j], sum2[SP + i]);
+            }
+          }
+        }
+        keep<V>(item, lane, u);
       }
       float sum[2 * SP], total[1];
 #pragma unroll
@@ -214,11 +203,12 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
     P2 sum_dP2[E::PAIRS ? SP * SP : 1] = {}, sum_e2[SP] = {}, sum_y2 = 0;
     float sum_dP[E::PAIRS ? 1 : SP * SP] = {};
     TX* dx = p.dx ? static_cast<TX*>(p.dx) + uint64_t(t) * uint32_t(S * C) : nullptr;
-    char* item = item0;
+    char *item = item0, *slot = ring;
+    if (WHOLE) slots_ready<ODD>();
 #pragma unroll 1
-    for (int c = c0, k = 0; k < K; ++k, c += GV, item += ITEM) {
+    for (int c = c0; c < c1; c += GV, item += ITEM, slot += NEXT_SLOT) {
       P2 du[H];
-      if (NEXT && c < C) {
+      if constexpr (NEXT) {
         P2 h[H], wn[H];
         const P2 r2 = twice(r_next), minus_k = twice(-k_next);
         kept<V>(item, lane, du);
@@ -233,12 +223,7 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
 #pragma unroll
         for (int j = 0; j < H; ++j) du[j] = fma2(mul2(r2, wn[j]), h[j], mul2(minus_k, du[j]));
       }
-      slot_ready<DEPTH, ODD>();
-      if (c >= C) {
-        copy_next();
-        if constexpr (DEPTH > 1) slot = slot == ring + (DEPTH - 1) * SLOT ? ring : slot + SLOT;
-        continue;
-      }
+      if (!WHOLE) slots_ready<ODD>();
       P2 D[SP][H], e[H], g[H];
 #pragma unroll
       for (int i = 0; i < SP; ++i) {
@@ -284,8 +269,11 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
       else
         RY::arrived_kept(slot + E::Y, lane, y, c, e, item + E::KY);
       if (gated) RY::arrived(slot + E::GATE, lane, gate, c, g);
-      copy_next();
-      if constexpr (DEPTH > 1) slot = slot == ring + (DEPTH - 1) * SLOT ? ring : slot + SLOT;
+      slot_read<ODD>();
+      {
+        const bool same = !WHOLE && c + GV < c1;
+        if (same || more) copy(!same, same ? t : t + step, WHOLE ? c : same ? c + GV : c0, slot);
+      }
       if (dx) {
 #pragma unroll
         for (int q = 0; q < SP; ++q) {
@@ -370,7 +358,7 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
     TY* dgate = gated && p.dgate ? static_cast<TY*>(p.dgate) + uint64_t(t) * uint32_t(C) : nullptr;
     item = item0;
 #pragma unroll 1
-    for (int c = c0; c < C; c += GV, item += ITEM) {
+    for (int c = c0; c < c1; c += GV, item += ITEM) {
       P2 yv[H], w[H], d[H];
       if (direct)
         RY::load(y, c, lane, C, yv);
@@ -399,7 +387,7 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
   if (!direct && (p.dw || (NEXT && p.dwn))) {
     __syncthreads();
     const int64_t row = int64_t(blockIdx.x) * pitch(C);
-    const char* first = smem + warp * p.warp_bytes + DEPTH * SLOT;
+    const char* first = smem + warp * p.warp_bytes + (WHOLE ? K : 1) * SLOT;
     if (p.dw) sum_shares<V, ODD>(first + E::KW, p, NG, ITEM, p.dw + row);
     if (NEXT && p.dwn) sum_shares<V, ODD>(first + E::KN, p, NG, ITEM, p.dwn + row);
   }
@@ -415,20 +403,28 @@ struct Backward {
     using E = LeaveBackward<SP, TX, TY, V, ODD, NEXT>;
     Params q = p;
     const bool mix = p.P.p != nullptr, gated = p.gate != nullptr;
-    const Shape sh = plan(q, shape_of(p.T, p.C, V, HCB_LEAVE_BWD_PER, 256), V, [&](int G, int direct) {
-      return Need{E::DEPTH * E::slot(mix, gated), E::item(gated, direct),
-                  4 * (G / 32 * E::Co::FLOATS + E::Sum::floats(G) + (NEXT ? E::SumNext::floats(G) : 0))};
-    });
+    auto need = [&](bool whole) {
+      return [&, whole](int G, int direct) {
+        const int slot = E::slot(mix, gated);
+        return Need{whole ? 0 : slot, E::item(gated, direct) + (whole ? slot : 0),
+                    4 * (G / 32 * E::Co::FLOATS + E::Sum::floats(G) + (NEXT ? E::SumNext::floats(G) : 0))};
+      };
+    };
+    const Shape want = shape_of(p.T, p.C, V, HCB_LEAVE_BWD_PER, 256);
     const int most = p.dw || p.dwn ? kMaxRows : 1 << 30;
-    const int w = EXACT && !q.direct && mix == (SP > 1) ? Weights::kind(p.w, NEXT ? p.wn : p.w) : 0;
+    int w = EXACT && mix == (SP > 1) ? Weights::kind(p.w, NEXT ? p.wn : p.w) : 0;
+    if (w == 2 && ODD) w = 0;
+    Shape sh = plan(q, want, V, need(w != 0 && SP <= HCB_LEAVE_BWD_WHOLE));
+    if (w != 0 && q.direct) w = 0;
+    if (w == 0) sh = plan(q, want, V, need(false));
     constexpr int W1 = EXACT ? 1 : 0, W2 = EXACT && !ODD ? 2 : 0;
     if (w == 1 && gated)
       return launch<leave_backward_kernel<SP, EXACT, TX, TY, V, ODD, NEXT, W1 ? 1 : 2, W1>>(q, sh, most, rows, s);
     if (w == 1)
       return launch<leave_backward_kernel<SP, EXACT, TX, TY, V, ODD, NEXT, W1 ? 0 : 2, W1>>(q, sh, most, rows, s);
-    if (w == 2 && W2 && gated)
+    if (w == 2 && gated)
       return launch<leave_backward_kernel<SP, W2 != 0, TX, TY, V, ODD, NEXT, W2 ? 1 : 2, W2>>(q, sh, most, rows, s);
-    if (w == 2 && W2)
+    if (w == 2)
       return launch<leave_backward_kernel<SP, W2 != 0, TX, TY, V, ODD, NEXT, W2 ? 0 : 2, W2>>(q, sh, most, rows, s);
     return launch<leave_backward_kernel<SP, false, TX, TY, V, ODD, NEXT, 2, 0>>(q, sh, most, rows, s);
   }
