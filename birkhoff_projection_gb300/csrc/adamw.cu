@@ -12,9 +12,11 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "adamw.h"
 #include "b4_device.cuh"
+#include "b4_pairs.cuh"
 #include "b4_types.h"
 
 namespace b4 {
@@ -23,15 +25,17 @@ int record_cuda_error(cudaError_t e);  // birkhoff4_api.cu
 
 namespace adamw {
 
+using namespace b4::pairs;
 using b4::bf16_t;
 
 constexpr int kThreads = 256;
-constexpr int kVec = 8;                    // elements of a thread at a time
-constexpr int kChunk = kThreads * kVec;    // elements of a CTA
-constexpr int kTable = 256;                // tensors of a launch at most
-constexpr float kTop = 448.0f;             // e4m3's largest number
-constexpr float kLeast = 0.001953125f;     // its smallest positive one, 2^-9
-static_assert(ADAMW_BLOCK % kVec == 0 && kChunk % ADAMW_BLOCK == 0 && ADAMW_BLOCK / kVec == 16, "");
+constexpr int kVec = 8;                          // neighbouring elements of a thread
+constexpr int kRuns = 2;                         // runs of kThreads kVec elements of a CTA
+constexpr int kChunk = kRuns * kThreads * kVec;  // elements of a CTA
+constexpr int kTable = 256;                      // tensors of a launch at most
+constexpr float kTop = 448.0f;                   // e4m3's largest number
+constexpr float kLeast = 0.001953125f;           // its smallest positive one, 2^-9
+static_assert(ADAMW_BLOCK % kVec == 0 && kThreads * kVec % ADAMW_BLOCK == 0 && ADAMW_BLOCK / kVec == 16, "");
 
 struct Entry {
   void* p;
@@ -53,133 +57,181 @@ struct Table {
 struct Hyper {
   float beta1, rest1, beta2, rest2;  // beta and 1 - beta
   float keep, rate, inv_root2, eps;  // 1 - lr wd, lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
+  float one;                         // 1
   const float* grad_scale;
 };
 
-// One element: the new moments (every product and sum rounded by itself) and
-// the new weight.
-__device__ __forceinline__ void update(const Hyper& h, float g, float& p, float& m, float& v, float& r) {
-  m = __fadd_rn(__fmul_rn(h.beta1, m), __fmul_rn(h.rest1, g));
-  v = __fadd_rn(__fmul_rn(h.beta2, v), __fmul_rn(h.rest2, __fmul_rn(g, g)));
-  r = __fsqrt_rn(v);
-  p = p * h.keep - h.rate * m / (r * h.inv_root2 + h.eps);
-}
-
+// Eight elements as they are in memory: 16 bytes to an fp32 quadruple, a bf16
+// octuple or (half of them) eight codes.  The loads of all of a thread's
+// arrays and runs are issued before the first is used.
 template <class T>
-__device__ __forceinline__ void load8(const void* base, int64_t i, int left, bool vec, float (&x)[kVec]) {
-  const T* p = static_cast<const T*>(base) + i;
-  if constexpr (sizeof(T) == 4) {
-    if (vec && left >= kVec) {
-      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) x[k] = k < left ? p[k] : 0.0f;
-    }
-  } else {
-    if (vec && left >= kVec) {
-      const uint4 q = *reinterpret_cast<const uint4*>(p);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[2 * k] = b4::bf16lo(w[k]), x[2 * k + 1] = b4::bf16hi(w[k]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) x[k] = k < left ? b4::bf16lo(p[k].bits) : 0.0f;
-    }
-  }
-}
-template <class T>
-__device__ __forceinline__ void store8(void* base, int64_t i, int left, bool vec, const float (&x)[kVec]) {
-  T* p = static_cast<T*>(base) + i;
-  if constexpr (sizeof(T) == 4) {
-    if (vec && left >= kVec) {
-      reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < kVec; ++k)
-        if (k < left) p[k] = x[k];
-    }
-  } else {
-    if (vec && left >= kVec) {
-      *reinterpret_cast<uint4*>(p) = make_uint4(b4::pack_bf16(x[0], x[1]), b4::pack_bf16(x[2], x[3]),
-                                                b4::pack_bf16(x[4], x[5]), b4::pack_bf16(x[6], x[7]));
-    } else {
-#pragma unroll
-      for (int k = 0; k < kVec; ++k)
-        if (k < left) p[k].bits = static_cast<uint16_t>(b4::pack_bf16(x[k], 0.0f));
-    }
-  }
-}
+struct Eight {
+  static constexpr int WORDS = 2 * sizeof(T);
+  uint32_t w[WORDS];
 
-// Eight e4m3 codes
-__device__ __forceinline__ void load_codes(const void* base, int64_t i, int left, bool vec, float scale,
-                                           float (&x)[kVec]) {
-  const uint8_t* p = static_cast<const uint8_t*>(base) + i;
-  uint32_t w[2] = {0, 0};
-  if (vec && left >= kVec) {
-    const uint2 q = *reinterpret_cast<const uint2*>(p);
-    w[0] = q.x, w[1] = q.y;
-  } else {
+  __device__ __forceinline__ void load(const void* base, int64_t i, int left, bool vec) {
+    const T* p = static_cast<const T*>(base) + i;
+    if (vec && left >= kVec) {
+      if constexpr (WORDS == 2) {
+        const uint2 q = *reinterpret_cast<const uint2*>(p);
+        w[0] = q.x, w[1] = q.y;
+      } else {
 #pragma unroll
-    for (int k = 0; k < kVec; ++k)
-      if (k < left) w[k / 4] |= static_cast<uint32_t>(p[k]) << (8 * (k % 4));
+        for (int k = 0; k < WORDS / 4; ++k) {
+          const uint4 q = reinterpret_cast<const uint4*>(p)[k];
+          w[4 * k] = q.x, w[4 * k + 1] = q.y, w[4 * k + 2] = q.z, w[4 * k + 3] = q.w;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < WORDS; ++k) w[k] = 0;
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) {
+        if (k < left) {
+          uint32_t x;
+          if constexpr (sizeof(T) == 4)
+            x = reinterpret_cast<const uint32_t*>(p)[k];
+          else if constexpr (sizeof(T) == 2)
+            x = reinterpret_cast<const uint16_t*>(p)[k];
+          else
+            x = reinterpret_cast<const uint8_t*>(p)[k];
+          w[k * sizeof(T) / 4] |= x << (8 * (k * sizeof(T) % 4));
+        }
+      }
+    }
   }
+  __device__ __forceinline__ void store(void* base, int64_t i, int left, bool vec) const {
+    T* p = static_cast<T*>(base) + i;
+    if (vec && left >= kVec) {
+      if constexpr (WORDS == 2) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < WORDS / 4; ++k)
+          reinterpret_cast<uint4*>(p)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) {
+        if (k < left) {
+          const uint32_t x = w[k * sizeof(T) / 4] >> (8 * (k * sizeof(T) % 4));
+          if constexpr (sizeof(T) == 4)
+            reinterpret_cast<uint32_t*>(p)[k] = x;
+          else if constexpr (sizeof(T) == 2)
+            reinterpret_cast<uint16_t*>(p)[k] = static_cast<uint16_t>(x);
+          else
+            reinterpret_cast<uint8_t*>(p)[k] = static_cast<uint8_t>(x);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void values(P2 (&x)[4]) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (sizeof(T) == 4)
+        x[k] = pair(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+      else
+        x[k] = pair(b4::bf16lo(w[k]), b4::bf16hi(w[k]));
+    }
+  }
+  __device__ __forceinline__ void round(const P2 (&x)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float lo, hi;
+      split(x[k], lo, hi);
+      if constexpr (sizeof(T) == 4)
+        w[2 * k] = __float_as_uint(lo), w[2 * k + 1] = __float_as_uint(hi);
+      else
+        w[k] = b4::pack_bf16(lo, hi);
+    }
+  }
+};
+
+// Eight e4m3 codes and their values.
+__device__ __forceinline__ void decode(const Eight<uint8_t>& c, float scale, P2 (&x)[4]) {
+  const P2 s = twice(scale);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     uint32_t h;  // two fp16, exact
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w[k / 2] >> (16 * (k % 2)))));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c.w[k / 2] >> (16 * (k % 2)))));
     float lo, hi;
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
         : "=f"(lo), "=f"(hi)
         : "r"(h));
-    x[2 * k] = __fmul_rn(lo, scale), x[2 * k + 1] = __fmul_rn(hi, scale);
+    x[k] = mul2(pair(lo, hi), s);
   }
 }
-__device__ __forceinline__ void store_codes(void* base, int64_t i, int left, bool vec, const float (&q)[kVec]) {
-  uint32_t w[2];
+
+// Maximum of magnitudes; NaN if one of them is.
+__device__ __forceinline__ float most_of(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
+// The codes and the scale of a block of which this thread has eight values,
+// 15 neighbours the others.
+template <bool ROOT>
+__device__ __forceinline__ float encode(const P2 (&x)[4], Eight<uint8_t>& c) {
+  float v[kVec];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) split(x[k], v[2 * k], v[2 * k + 1]);
+  float most = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) most = most_of(most, v[k]);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) most = most_of(most, __shfl_xor_sync(0xffffffffu, most, o));
+  const bool finite = most < INFINITY;
+  if (__any_sync(0xffffffffu, !finite)) {  // NaN and infinities do not count
+    float some = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) some = fmaxf(some, fabsf(v[k]) < INFINITY ? fabsf(v[k]) : 0.0f);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) some = fmaxf(some, __shfl_xor_sync(0xffffffffu, some, o));
+    most = some;
+  }
+  // below about 2^-119 the factor would overflow: held at 3e38, it stores such a block's values smaller
+  const float inv = most > 0.0f ? fminf(__fmul_rn(kTop, __frcp_rn(most)), 3.0e38f) : 0.0f;
+  float q[kVec];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) split(mul2(x[k], twice(inv)), q[2 * k], q[2 * k + 1]);
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) {
+    if constexpr (ROOT) q[k] = v[k] > 0.0f ? fmaxf(q[k], kLeast) : q[k];
+    if (!finite && !(fabsf(v[k]) < INFINITY)) q[k] = NAN;
+  }
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     uint16_t lo, hi;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(q[4 * k + 1]), "f"(q[4 * k]));
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(q[4 * k + 3]), "f"(q[4 * k + 2]));
-    w[k] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
-  }
-  uint8_t* p = static_cast<uint8_t*>(base) + i;
-  if (vec && left >= kVec) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-  } else {
-#pragma unroll
-    for (int k = 0; k < kVec; ++k)
-      if (k < left) p[k] = static_cast<uint8_t>(w[k / 4] >> (8 * (k % 4)));
-  }
-}
-
-// The scale of a block from the magnitudes of its 16 threads, and its
-// values' codes before rounding.
-__device__ __forceinline__ float encode(float (&x)[kVec], bool root) {
-  float most = 0.0f;
-#pragma unroll
-  for (int k = 0; k < kVec; ++k) {
-    const float a = fabsf(x[k]);
-    most = fmaxf(most, a < INFINITY ? a : 0.0f);  // NaN and infinities do not count
-  }
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  // below about 2^-119 the factor would overflow: held at 3e38, it stores such a block's values smaller
-  const float inv = most > 0.0f ? fminf(__fmul_rn(kTop, __frcp_rn(most)), 3.0e38f) : 0.0f;
-#pragma unroll
-  for (int k = 0; k < kVec; ++k) {
-    float q = __fmul_rn(x[k], inv);
-    if (root && x[k] > 0.0f) q = fmaxf(q, kLeast);
-    if (!(fabsf(x[k]) < INFINITY)) q = NAN;
-    x[k] = q;
+    c.w[k] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
   }
   return __fmul_rn(most, 1.0f / kTop);
 }
 
+// New moments and weights of eight elements.  The moments' products and sums
+// are each rounded: a packed product and a packed sum are fused where they
+// meet, so the sum is one product times 1 (a 1 that only the launch knows)
+// plus the other, which rounds once and is the same number.  r is sqrt(v).
+__device__ __forceinline__ void update(const Hyper& h, P2 (&g)[4], P2 (&p)[4], P2 (&m)[4], P2 (&v)[4], P2 (&r)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    m[k] = fma2(mul2(twice(h.beta1), m[k]), twice(h.one), mul2(twice(h.rest1), g[k]));
+    v[k] = fma2(mul2(twice(h.beta2), v[k]), twice(h.one), mul2(twice(h.rest2), mul2(g[k], g[k])));
+    float lo, hi;
+    split(v[k], lo, hi);
+    r[k] = pair(__fsqrt_rn(lo), __fsqrt_rn(hi));
+    split(fma2(r[k], twice(h.inv_root2), twice(h.eps)), lo, hi);
+    const P2 up = mul2(mul2(m[k], twice(-h.rate)), pair(b4::rcp(lo), b4::rcp(hi)));
+    p[k] = fma2(p[k], twice(h.keep), up);
+  }
+}
+
 template <class TP, class TG, bool MASTER, bool EIGHT, int N>
 __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ Table<N> t, const Hyper h) {
+  using TW = std::conditional_t<MASTER, float, TP>;        // what the step is taken on
+  using TS = std::conditional_t<EIGHT, uint8_t, float>;    // a moment's elements
   const uint32_t chunk = blockIdx.x;
   int lo = 0, hi = t.count;  // the last tensor whose first chunk is at most `chunk`
   while (hi - lo > 1) {
@@ -191,46 +243,69 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
   }
   const Entry& x = t.at[lo];
   const bool vec = x.vec != 0;
-  const int64_t i = int64_t(chunk - t.first[lo]) * kChunk + threadIdx.x * kVec;
-  const int64_t rest = x.n - i;
-  const int left = rest > kVec ? kVec : rest < 0 ? 0 : static_cast<int>(rest);
-  float g[kVec], p[kVec], m[kVec], v[kVec];
-  load8<TG>(x.g, i, left, vec, g);
-  if constexpr (MASTER)
-    load8<float>(x.master, i, left, vec, p);
-  else
-    load8<TP>(x.p, i, left, vec, p);
-  if constexpr (EIGHT) {
-    const int64_t block = i / ADAMW_BLOCK;
-    load_codes(x.m, i, left, vec, left > 0 ? x.m_scale[block] : 0.0f, m);
-    load_codes(x.v, i, left, vec, left > 0 ? x.v_scale[block] : 0.0f, v);
+  const int64_t i0 = int64_t(chunk - t.first[lo]) * kChunk + threadIdx.x * kVec;
+  void* weights = MASTER ? static_cast<void*>(x.master) : x.p;
+
+  Eight<TG> g8[kRuns];
+  Eight<TW> p8[kRuns];
+  Eight<TS> m8[kRuns], v8[kRuns];
+  float ms[kRuns], vs[kRuns];
+  int left[kRuns];
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) v[j] = __fmul_rn(v[j], v[j]);
-  } else {
-    load8<float>(x.m, i, left, vec, m);
-    load8<float>(x.v, i, left, vec, v);
-  }
-  if (h.grad_scale) {
-    const float s = *h.grad_scale;
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) g[j] *= s;
-  }
-  float r[kVec];
-#pragma unroll
-  for (int j = 0; j < kVec; ++j) update(h, g[j], p[j], m[j], v[j], r[j]);
-  if constexpr (MASTER) store8<float>(x.master, i, left, vec, p);
-  store8<TP>(x.p, i, left, vec, p);
-  if constexpr (EIGHT) {
-    const float ms = encode(m, false), vs = encode(r, true);
-    store_codes(x.m, i, left, vec, m);
-    store_codes(x.v, i, left, vec, r);
-    if (left > 0 && threadIdx.x % (ADAMW_BLOCK / kVec) == 0) {
-      x.m_scale[i / ADAMW_BLOCK] = ms;
-      x.v_scale[i / ADAMW_BLOCK] = vs;
+  for (int a = 0; a < kRuns; ++a) {
+    const int64_t i = i0 + a * kThreads * kVec, rest = x.n - i;
+    left[a] = rest > kVec ? kVec : rest < 0 ? 0 : static_cast<int>(rest);
+    g8[a].load(x.g, i, left[a], vec);
+    p8[a].load(weights, i, left[a], vec);
+    m8[a].load(x.m, i, left[a], vec);
+    v8[a].load(x.v, i, left[a], vec);
+    if constexpr (EIGHT) {
+      ms[a] = left[a] > 0 ? x.m_scale[i / ADAMW_BLOCK] : 0.0f;
+      vs[a] = left[a] > 0 ? x.v_scale[i / ADAMW_BLOCK] : 0.0f;
     }
-  } else {
-    store8<float>(x.m, i, left, vec, m);
-    store8<float>(x.v, i, left, vec, v);
+  }
+  const float gs = h.grad_scale ? *h.grad_scale : 1.0f;
+#pragma unroll
+  for (int a = 0; a < kRuns; ++a) {
+    const int64_t i = i0 + a * kThreads * kVec;
+    P2 g[4], p[4], m[4], v[4], r[4];
+    g8[a].values(g);
+    p8[a].values(p);
+    if constexpr (EIGHT) {
+      decode(m8[a], ms[a], m);
+      decode(v8[a], vs[a], v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = mul2(v[k], v[k]);
+    } else {
+      m8[a].values(m);
+      v8[a].values(v);
+    }
+    if (h.grad_scale) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) g[k] = mul2(g[k], twice(gs));
+    }
+    update(h, g, p, m, v, r);
+    p8[a].round(p);
+    p8[a].store(weights, i, left[a], vec);
+    if constexpr (MASTER) {
+      Eight<TP> copy;
+      copy.round(p);
+      copy.store(x.p, i, left[a], vec);
+    }
+    if constexpr (EIGHT) {
+      const float mscale = encode<false>(m, m8[a]), vscale = encode<true>(r, v8[a]);
+      m8[a].store(x.m, i, left[a], vec);
+      v8[a].store(x.v, i, left[a], vec);
+      if (left[a] > 0 && threadIdx.x % (ADAMW_BLOCK / kVec) == 0) {
+        x.m_scale[i / ADAMW_BLOCK] = mscale;
+        x.v_scale[i / ADAMW_BLOCK] = vscale;
+      }
+    } else {
+      m8[a].round(m);
+      v8[a].round(v);
+      m8[a].store(x.m, i, left[a], vec);
+      v8[a].store(x.v, i, left[a], vec);
+    }
   }
 }
 
@@ -311,6 +386,7 @@ extern "C" int adamw_step(const adamw_tensor* x, int32_t count, const adamw_opts
   h.rate = static_cast<float>(o->lr / (1.0 - std::pow(o->beta1, t)));
   h.inv_root2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(o->beta2, t)));
   h.eps = static_cast<float>(o->eps);
+  h.one = 1.0f;
   h.grad_scale = o->grad_scale;
 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
