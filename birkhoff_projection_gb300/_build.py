@@ -2,6 +2,8 @@
 
 The kernel translation units compile in parallel; the shared library links
 the CUDA runtime statically, so it needs nothing from PyTorch at load time.
+Beside it, g++ builds a small extension module against PyTorch's headers, the
+short way from Python into the library's block and optimizer entry points.
 
     python -m birkhoff_projection_gb300._build [--force] [-v]
 """
@@ -10,6 +12,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libbirkhoff4.so")
+BINDING_PATH = os.path.join(PKG, "_block_binding.so")
+BINDING_SOURCE = os.path.join(CSRC, "block_binding.cpp")
 
 SOURCES = ["birkhoff4_api.cu", "k_forward.cu", "k_backward.cu", "k_fused.cu", "k_sinkhorn.cu",
            "birkhoff4_noalloc.cu", "k_nxn.cu", "eot_stream.cu",
@@ -40,10 +45,34 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
     return all(os.path.getmtime(d) <= t for d in _inputs())
+
+
+def _run(cmd, what: str, verbose: bool = False) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed:\n%s%s" % (what, r.stdout, r.stderr))
+    if verbose:
+        sys.stderr.write(r.stdout + r.stderr)
+
+
+def _build_binding(verbose: bool) -> None:
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.isabs(nvcc()) else "/usr/local/cuda"
+    include = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = BINDING_PATH + ".tmp%d" % os.getpid()
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
+         + ["-I" + d for d in include] + [BINDING_SOURCE, "-o", tmp, "-L" + lib, "-Wl,-rpath," + lib,
+                                          "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"],
+         "g++ of block_binding.cpp", verbose)
+    os.replace(tmp, BINDING_PATH)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -58,21 +87,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     def compile_one(src):
         obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
-        cmd = [nvcc()] + ARCH + NVCC_FLAGS + extra + ["-c", os.path.join(CSRC, src), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError("nvcc failed for %s:\n%s%s" % (src, r.stdout, r.stderr))
-        if verbose:
-            sys.stderr.write(r.stdout + r.stderr)
+        _run([nvcc()] + ARCH + NVCC_FLAGS + extra + ["-c", os.path.join(CSRC, src), "-o", obj], "nvcc of " + src, verbose)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_build_binding, verbose)
         objs = list(ex.map(compile_one, SOURCES))
+        binding.result()
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
-    cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("nvcc link failed:\n%s%s" % (r.stdout, r.stderr))
+    _run([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs, "nvcc link")
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

@@ -6,6 +6,8 @@ loaded, every call raises: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -138,6 +140,25 @@ def lib():
             fn.argtypes = args
         _lib = handle
         return handle
+
+
+_binding = None
+
+
+def binding():
+    """The extension module that makes the plain calls of the block and
+    optimizer entry points (built with the library; loaded on first use)."""
+    global _binding
+    if _binding is None:
+        handle = lib()
+        loader = importlib.machinery.ExtensionFileLoader("_block_binding", _build.BINDING_PATH)
+        spec = importlib.util.spec_from_loader("_block_binding", loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        module.init(*[ctypes.cast(getattr(handle, name), ctypes.c_void_p).value for name in (
+            "hcb_enter", "hcb_enter_backward", "hcb_leave", "hcb_leave_backward", "hcb_workspace_bytes")])
+        _binding = module
+    return _binding
 
 
 def library_path() -> str:

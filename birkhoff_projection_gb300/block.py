@@ -43,6 +43,17 @@ _ARGS = struct.Struct("<q11i3f12Q14q11QQ")
 _NONE = (None, 0, 0, 0)  # a tensor that is not there: itself, address, type, stride
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _functions = {}
+_module = None
+
+
+def _plain():
+    """The extension module for plain arguments (contiguous tensors on the
+    current device): its functions return None where anything else is asked
+    or is wrong, and the code here does the call in full."""
+    global _module
+    if _module is None:
+        _module = _lib.binding()
+    return _module
 
 
 def _call(name, dev, args):
@@ -184,6 +195,9 @@ def workspace_bytes(tokens: int, channels: int, weights: int = 1) -> int:
 
 
 def _enter(x, a, weight, eps, out_dtype):
+    h = _plain().enter(x, a, weight, eps, -1 if out_dtype is None else _DT.get(out_dtype, 2))
+    if h is not None:
+        return h
     shape, lead, T, S, C, dev = _x(x)
     dtype = out_dtype or x.dtype
     yk = _y_type(dtype, x, "out_dtype")
@@ -205,6 +219,10 @@ def enter_backward(dh: torch.Tensor, x: torch.Tensor, a: torch.Tensor = None, we
     a and weight are.  dres, shaped like x, is added to dx: the gradient that
     the streams have from elsewhere.  workspace: a uint8 tensor of
     workspace_bytes (allocated here if not given)."""
+    if workspace is None:
+        got = _plain().enter_backward(dh, x, a, weight, eps, dres)
+        if got is not None:
+            return EnterGrads._make(got)
     shape, lead, T, S, C, dev = _x(x)
     if not isinstance(dh, torch.Tensor):
         _wrong(dh, "dh", None, None, None)
@@ -229,6 +247,10 @@ def enter_backward(dh: torch.Tensor, x: torch.Tensor, a: torch.Tensor = None, we
 
 
 def _leave(x, y, P, b, gate, act, weight, norm, scale, eps, want_h, a_next, weight_next, eps_next):
+    got = _plain().leave(x, y, P, b, gate, _ACT.get(act, -1), weight, norm, scale, eps, want_h, a_next, weight_next,
+                         eps_next)
+    if got is not None:
+        return got
     shape, lead, T, S, C, dev = _x(x)
     if not isinstance(y, torch.Tensor):
         _wrong(y, "y", None, None, None)
@@ -258,6 +280,11 @@ def _leave(x, y, P, b, gate, act, weight, norm, scale, eps, want_h, a_next, weig
 
 def _leave_backward(dout, dh, out, x, y, P, b, gate, act, weight, norm, scale, eps, a_next, weight_next, eps_next,
                     workspace):
+    if workspace is None:
+        got = _plain().leave_backward(x, y, P, b, gate, _ACT.get(act, -1), weight, norm, scale, eps, dout, dh, out,
+                                      a_next, weight_next, eps_next)
+        if got is not None:
+            return got
     shape, lead, T, S, C, dev = _x(x)
     if not isinstance(y, torch.Tensor):
         _wrong(y, "y", None, None, None)
@@ -294,7 +321,7 @@ def _leave_backward(dout, dh, out, x, y, P, b, gate, act, weight, norm, scale, e
         xp, yp, gp, Pp, ap, bp, wp, wnp, dop, hp, 0, op,
         x_ts, x_ss, y_ts, g_ts, P_ts, a_ts, b_ts, do_ts, do_ss, h_ts, 0, 0, o_ts, o_ss,
         0, 0, dxp, dyp, dgp, dPp, dap, dbp, dwp, dwnp, wsp, ws))
-    return (dx, dy, dP, db, dgate, dw), da, dwn
+    return dx, dy, dP, db, dgate, dw, da, dwn
 
 
 def leave_backward(dout: torch.Tensor, x: torch.Tensor, y: torch.Tensor, P: torch.Tensor = None,
@@ -303,8 +330,8 @@ def leave_backward(dout: torch.Tensor, x: torch.Tensor, y: torch.Tensor, P: torc
                    workspace: torch.Tensor = None) -> LeaveGrads:
     """The gradients of leave: (dx, dy, dP, db, dgate, dweight), None where
     the tensor is.  Without P, dx is dout itself."""
-    return LeaveGrads(*_leave_backward(dout, None, None, x, y, P, b, gate, act, weight, norm, scale, eps, None, None,
-                                       0.0, workspace)[0])
+    return LeaveGrads._make(_leave_backward(dout, None, None, x, y, P, b, gate, act, weight, norm, scale, eps, None, None,
+                                            0.0, workspace)[:6])
 
 
 def leave_enter_backward(dout: torch.Tensor, dh: torch.Tensor, out: torch.Tensor, x: torch.Tensor, y: torch.Tensor,
@@ -315,9 +342,8 @@ def leave_enter_backward(dout: torch.Tensor, dh: torch.Tensor, out: torch.Tensor
     """The gradients of leave_enter, from those of both its results and its
     stored result `out`, in one pass: (dx, dy, dP, db, dgate, dweight,
     da_next, dweight_next), None where the tensor is."""
-    got, da, dwn = _leave_backward(dout, dh, out, x, y, P, b, gate, act, weight, norm, scale, eps, a_next, weight_next,
-                                   eps_next, workspace)
-    return LeaveEnterGrads(*got, da, dwn)
+    return LeaveEnterGrads._make(_leave_backward(dout, dh, out, x, y, P, b, gate, act, weight, norm, scale, eps, a_next,
+                                                 weight_next, eps_next, workspace))
 
 
 class _Enter(torch.autograd.Function):
@@ -337,7 +363,7 @@ class _Enter(torch.autograd.Function):
 class _Leave(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, y, P, b, gate, weight, *how):
-        ctx.save_for_backward(x, y, P, b, gate, weight)
+        ctx.save_for_backward(None if P is None else x, y, P, b, gate, weight)
         ctx.how = how
         act, norm, scale, eps = how
         return _leave(x, y, P, b, gate, act, weight, norm, scale, eps, False, None, None, 0.0)[0]
@@ -347,7 +373,7 @@ class _Leave(torch.autograd.Function):
     def backward(ctx, dout):
         x, y, P, b, gate, weight = ctx.saved_tensors
         act, norm, scale, eps = ctx.how
-        g = leave_backward(dout, x, y, P, b, gate=gate, act=act, weight=weight, norm=norm, scale=scale, eps=eps)
+        g = leave_backward(dout, dout if x is None else x, y, P, b, gate=gate, act=act, weight=weight, norm=norm, scale=scale, eps=eps)
         return (g.dx, g.dy, g.dP, g.db, g.dgate, g.dweight, None, None, None, None)
 
 
@@ -356,7 +382,8 @@ class _LeaveEnter(torch.autograd.Function):
     def forward(ctx, x, y, P, b, gate, weight, a_next, weight_next, *how):
         act, norm, scale, eps, eps_next = how
         out, h = _leave(x, y, P, b, gate, act, weight, norm, scale, eps, True, a_next, weight_next, eps_next)
-        ctx.save_for_backward(x, y, P, b, gate, weight, a_next, weight_next, out)
+        # without a mixing matrix the gradients do not need x's values
+        ctx.save_for_backward(None if P is None else x, y, P, b, gate, weight, a_next, weight_next, out)
         ctx.how = how
         return out, h
 
@@ -365,7 +392,7 @@ class _LeaveEnter(torch.autograd.Function):
     def backward(ctx, dout, dh):
         x, y, P, b, gate, weight, a_next, weight_next, out = ctx.saved_tensors
         act, norm, scale, eps, eps_next = ctx.how
-        g = leave_enter_backward(dout, dh, out, x, y, P, b, gate=gate, act=act, weight=weight, norm=norm, scale=scale,
+        g = leave_enter_backward(dout, dh, out, out if x is None else x, y, P, b, gate=gate, act=act, weight=weight, norm=norm, scale=scale,
                                  eps=eps, a_next=a_next, weight_next=weight_next, eps_next=eps_next)
         return (g.dx, g.dy, g.dP, g.db, g.dgate, g.dweight, g.da_next, g.dweight_next, None, None, None, None, None)
 
@@ -386,6 +413,9 @@ def enter(x: torch.Tensor, a: torch.Tensor = None, weight: torch.Tensor = None, 
 
     a [..., S]: the read coefficients (ones if None); weight [C] (ones if
     None); out_dtype: h's type (x's if None; x fp32 may give bf16)."""
+    h = _plain().enter(x, a, weight, eps, -1 if out_dtype is None else _DT.get(out_dtype, 2))
+    if h is not None:
+        return h
     if _learns(x, a, weight):
         return _Enter.apply(x, a, weight, eps, out_dtype)
     return _enter(x, a, weight, eps, out_dtype)
@@ -402,6 +432,9 @@ def leave(x: torch.Tensor, y: torch.Tensor, P: torch.Tensor = None, b: torch.Ten
     None); b [..., S]: the write coefficients (ones if None); gate [..., C]
     of y's type with act "sigmoid", "silu" or "linear" (no gate if None);
     weight [C] (ones if None)."""
+    got = _plain().leave(x, y, P, b, gate, _ACT.get(act, -1), weight, norm, scale, eps, False, None, None, 0.0)
+    if got is not None:
+        return got[0]
     if _learns(x, y, P, b, gate, weight):
         return _Leave.apply(x, y, P, b, gate, weight, act, norm, scale, eps)
     return _leave(x, y, P, b, gate, act, weight, norm, scale, eps, False, None, None, 0.0)[0]
@@ -417,6 +450,10 @@ def leave_enter(x: torch.Tensor, y: torch.Tensor, P: torch.Tensor = None, b: tor
 
     For a residual of one stream: x' = x + scale * act(gate) * norm(y), and
     the norm of x'."""
+    got = _plain().leave(x, y, P, b, gate, _ACT.get(act, -1), weight, norm, scale, eps, True, a_next, weight_next,
+                         eps_next)
+    if got is not None:
+        return got
     if _learns(x, y, P, b, gate, weight, a_next, weight_next):
         return _LeaveEnter.apply(x, y, P, b, gate, weight, a_next, weight_next, act, norm, scale, eps, eps_next)
     return _leave(x, y, P, b, gate, act, weight, norm, scale, eps, True, a_next, weight_next, eps_next)

@@ -16,9 +16,10 @@ import struct
 from array import array
 
 import torch
+from torch.optim import optimizer as _hooks
 
 from . import _DT
-from ._lib import ADAMW_BLOCK, check, lib
+from ._lib import ADAMW_BLOCK, binding, check, lib
 
 __all__ = ["AdamW"]
 
@@ -41,11 +42,7 @@ class AdamW(torch.optim.Optimizer):
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 1e-2, *,
                  state_bits: int = 32, master_weights: bool = False):
-        for name, v in (("lr", lr), ("eps", eps), ("weight_decay", weight_decay)):
-            if not 0.0 <= v < float("inf"):
-                raise ValueError("%s must be finite and not negative, got %r" % (name, v))
-        if len(betas) != 2 or not all(0.0 <= b < 1.0 for b in betas):
-            raise ValueError("betas must be two numbers in [0, 1), got %r" % (betas,))
+        self._check(lr, betas, eps, weight_decay)
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32, got %r" % (state_bits,))
         self.steps = 0
@@ -54,6 +51,15 @@ class AdamW(torch.optim.Optimizer):
         super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay))
         self._ready = True
         self._pack()
+
+    @staticmethod
+    def _check(lr, betas, eps, weight_decay):
+        inf = float("inf")
+        if not (0.0 <= lr < inf and 0.0 <= eps < inf and 0.0 <= weight_decay < inf):
+            raise ValueError("invalid lr, eps or weight_decay (finite and not negative): %r, %r, %r"
+                             % (lr, eps, weight_decay))
+        if len(betas) != 2 or not (0.0 <= betas[0] < 1.0 and 0.0 <= betas[1] < 1.0):
+            raise ValueError("betas must be two numbers in [0, 1), got %r" % (betas,))
 
     def add_param_group(self, group):
         if self._ready:
@@ -122,7 +128,7 @@ class AdamW(torch.optim.Optimizer):
                                  s["exp_avg_scale"].data_ptr() if eight else 0,
                                  s["exp_avg_sq_root_scale"].data_ptr() if eight else 0,
                                  s["master"].data_ptr() if master else 0, p.numel()))
-                self._plans.append((group, dtype, params, rows))
+                self._plans.append((group, dtype, params, rows, rows.tobytes()))
 
     def packed(self) -> dict:
         """The packed state buffers: exp_avg and exp_avg_sq (32 bits), or
@@ -132,9 +138,18 @@ class AdamW(torch.optim.Optimizer):
         multiple of 128 elements."""
         return dict(self._packed)
 
-    @torch.no_grad()
     def step(self, closure=None, *, grad_scale: torch.Tensor = None):
         """One step on the parameters' gradients (fp32 or bf16, contiguous)."""
+        # torch's wrapper of a step, for its hooks and the profiler's mark, takes
+        # longer than a small step: only where there is use for it
+        if (self._optimizer_step_pre_hooks or self._optimizer_step_post_hooks or _hooks._global_optimizer_pre_hooks
+                or _hooks._global_optimizer_post_hooks or torch.autograd._profiler_enabled()):
+            return self._marked_step(self, closure, grad_scale=grad_scale)
+        return self._step(closure, grad_scale=grad_scale)
+
+    step.hooked = True  # torch.optim.Optimizer leaves it as it is
+
+    def _step(self, closure=None, *, grad_scale=None):
         loss = None
         if closure is not None:
             with torch.enable_grad():
@@ -144,7 +159,12 @@ class AdamW(torch.optim.Optimizer):
             raise ValueError("grad_scale must be one float32 on %s" % self._device)
         dev = self._device.index
         calls = []  # the tables, and whatever they point to that is not kept elsewhere
-        for group, dtype, params, rows in self._plans:
+        plain = binding().adamw_table
+        for group, dtype, params, rows, packed in self._plans:
+            got = plain(params, packed, _DT[dtype], dev)  # None where the gradients are not all plain
+            if got is not None:
+                calls.append((group, _DT[dtype], got[1], got[0], None))
+                continue
             grads = [p.grad for p in params]
             if any([g is None for g in grads]):  # (`in` would compare tensors)
                 some = [k for k, g in enumerate(grads) if g is not None]
@@ -156,6 +176,11 @@ class AdamW(torch.optim.Optimizer):
             if not kinds <= _DT.keys() or {g.get_device() for g in grads} != {dev} \
                     or {g.layout for g in grads} != {torch.strided}:
                 raise ValueError("gradients must be dense float32 or bfloat16 tensors on %s" % self._device)
+            for k, (p, g) in enumerate(zip(params, grads)):
+                if p.dtype != dtype or p.get_device() != dev or not p.is_contiguous() \
+                        or not p.numel() == g.numel() == rows[(k + 1) * _FIELDS - 1]:
+                    raise ValueError("parameters must stay as they were at construction: contiguous, of one type and "
+                                     "size, on %s" % self._device)
             if not all([g.is_contiguous() for g in grads]):
                 grads = [g.contiguous() for g in grads]
             table = rows[:]
@@ -168,18 +193,27 @@ class AdamW(torch.optim.Optimizer):
                                        for v in table[k * _FIELDS:(k + 1) * _FIELDS]])
                 else:
                     mine = table
-                calls.append((group, dtype, kind, mine, grads))
-        self.steps += 1
+                calls.append((group, _DT[dtype], _DT[kind], mine.tobytes(), grads))
+        for group, *_ in calls:  # before the first launch
+            self._check(group["lr"], group["betas"], group["eps"], group["weight_decay"])
         scale = 0 if grad_scale is None else grad_scale.data_ptr()
-        f = lib().adamw_step
-        with torch.cuda.device(self._device):
-            stream = torch._C._cuda_getCurrentRawStream(dev)
-            for group, dtype, kind, table, _ in calls:
-                beta1, beta2 = group["betas"]
-                opts = _OPTS.pack(_DT[dtype], _DT[kind], self.state_bits, group["lr"], beta1, beta2, group["eps"],
-                                  group["weight_decay"], self.steps, scale)
-                check(f(table.buffer_info()[0], len(table) // _FIELDS, opts, stream), "adamw_step")
+        if dev == torch.cuda.current_device():
+            self._launch(calls, scale)
+        else:
+            with torch.cuda.device(dev):
+                self._launch(calls, scale)
+        self.steps += 1
         return loss
+
+    def _launch(self, calls, scale):
+        f, stream = lib().adamw_step, torch._C._cuda_getCurrentRawStream(self._device.index)
+        for group, p_type, g_type, table, _ in calls:
+            beta1, beta2 = group["betas"]
+            opts = _OPTS.pack(p_type, g_type, self.state_bits, group["lr"], beta1, beta2, group["eps"],
+                              group["weight_decay"], self.steps + 1, scale)
+            check(f(table, len(table) // (8 * _FIELDS), opts, stream), "adamw_step")
+
+    _marked_step = staticmethod(torch.optim.Optimizer.profile_hook_step(_step))
 
     def state_dict(self):
         d = super().state_dict()

@@ -173,6 +173,22 @@ def test_adamw_refusals(L):
     assert step(L, {"n": 0, "p": None}) == B4_OK  # no elements: nothing to do
 
 
+def test_the_short_way_takes_nothing_that_is_not_plain():
+    m = _lib.binding()
+    x = torch.zeros(3, 4, 8)
+    y = torch.zeros(3, 8)
+    for bad in (x, None, 1, "x", [x]):
+        assert m.enter(bad, None, None, 1e-6, -1) is None
+        assert m.enter_backward(y, bad, None, None, 1e-6, None) is None
+        assert m.leave(bad, y, None, None, None, 1, None, True, 1.0, 1e-6, False, None, None, 0.0) is None
+        assert m.leave_backward(bad, y, None, None, None, 1, None, True, 1.0, 1e-6, x, None, None, None, None, 0.0) is None
+    assert m.adamw_table([x], b"", 0, 0) is None and m.adamw_table([], b"", 0, 0) is None
+    assert m.adamw_table([x], bytes(64), 0, 0) is None and m.adamw_table((x,), bytes(64), 0, 0) is None
+    for f in (m.enter, m.enter_backward, m.leave, m.leave_backward, m.adamw_table, m.init):
+        with pytest.raises(TypeError):
+            f(x)
+
+
 def test_python_refuses_tensors_off_the_gpu():
     x, y = torch.zeros(3, 4, 8), torch.zeros(3, 8)
     for f in (lambda: block.enter(x), lambda: block.leave(x, y), lambda: block.leave_enter(x, y),

@@ -93,7 +93,7 @@ def test_steps(dtype, gtype, master, bits):
                 p.grad = g
             opt.step()
         else:  # a parameter's .grad has its type: the C entry takes any pair
-            (_, _, some, rows), = opt._plans
+            (_, _, some, rows, _), = opt._plans
             some_grads = [g for g in grads if g.numel()]
             table = (_lib.AdamwTensor * len(some))(*[
                 _lib.AdamwTensor(p.data_ptr(), g.data_ptr(), *rows[8 * k + 2:8 * k + 8])
@@ -256,7 +256,54 @@ def test_refusals():
     opt.param_groups[0]["lr"] = -1.0
     with pytest.raises(Exception, match="invalid"):
         opt.step()
-    assert torch.equal(params[0].detach(), before)
+    assert torch.equal(params[0].detach(), before) and opt.steps == 0
+    opt.param_groups[0]["lr"] = 1.0
+    params[0].data = torch.zeros(5, device=DEV)
+    params[0].grad = torch.ones(5, device=DEV)
+    with pytest.raises(ValueError, match="construction"):
+        opt.step()
+
+
+def test_a_bad_group_stops_every_group():
+    params = [torch.nn.Parameter(torch.ones(9, device=DEV)) for _ in range(2)]
+    opt = optim.AdamW([{"params": params[:1]}, {"params": params[1:]}])
+    for p in params:
+        p.grad = torch.ones(9, device=DEV)
+    opt.param_groups[1]["betas"] = (0.9, 1.5)
+    with pytest.raises(ValueError, match="betas"):
+        opt.step()
+    assert all((p == 1).all() for p in params) and opt.steps == 0
+
+
+def test_gradients_that_are_not_contiguous():
+    p = torch.nn.Parameter(rnd(1, 6, 8).to(DEV))
+    q = torch.nn.Parameter(p.detach().clone())
+    a, b = optim.AdamW([p], **HYPER), optim.AdamW([q], **HYPER)
+    g = rnd(2, 8, 6).to(DEV)
+    p.grad, q.grad = g.t(), g.t().contiguous()
+    assert not p.grad.is_contiguous()
+    a.step(), b.step()
+    assert torch.equal(p, q)
+
+
+def test_hooks_profiler_and_schedulers():
+    p = torch.nn.Parameter(torch.ones(9, device=DEV))
+    opt = optim.AdamW([p], lr=1.0)
+    p.grad = torch.ones(9, device=DEV)
+    seen = []
+    handles = [opt.register_step_pre_hook(lambda *a: seen.append("before")), opt.register_step_post_hook(lambda *a: seen.append("after"))]
+    opt.step()
+    assert seen == ["before", "after"] and opt.steps == 1
+    for h in handles:
+        h.remove()
+    sched = torch.optim.lr_scheduler.LambdaLR(opt, lambda n: 0.5 ** n)
+    before = p.detach().clone()
+    assert opt.step(lambda: torch.tensor(3.0)) == 3.0
+    sched.step()
+    assert opt.param_groups[0]["lr"] == 0.5 and opt.steps == 2 and not torch.equal(p, before) and len(seen) == 2
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CPU]) as prof:
+        opt.step()
+    assert any("AdamW.step" in e.key for e in prof.key_averages()) and opt.steps == 3
 
 
 def test_captured_in_a_graph():

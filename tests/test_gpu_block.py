@@ -192,6 +192,37 @@ def test_vector_and_element_paths_agree():
     assert (a != b).float().mean() < 1e-2 and (a.float() - b.float()).abs().max() <= 2.0 ** -6 * a.float().abs().max()
 
 
+def test_plain_and_full_calls_agree(monkeypatch):
+    """The extension module's short way and the Python code make the same calls."""
+    class Nothing:
+        def __getattr__(self, name):
+            return lambda *args: None
+
+    def results():
+        got = []
+        for S, tx, ty, coef, weight, act in ((4, H, H, F, F, "silu"), (1, F, H, F, H, None), (3, F, F, H, F, "linear")):
+            for mix in (True, False):
+                k = inputs(7, S, 88, tx, ty, act, mix, coef, weight)
+                how = dict(gate=k["gate"], act=act or "sigmoid", weight=k["w"], norm=act != "linear", scale=0.25, eps=1e-5)
+                nxt = dict(a_next=k["a"], weight_next=k["w2"], eps_next=1e-4)
+                got.append(block.enter(k["x"], k["a"], k["w"], eps=1e-3, out_dtype=ty))
+                got += block.enter_backward(k["dh"], k["x"], k["a"], k["w"], eps=1e-3, dres=k["D"])
+                got += block.enter_backward(k["dh"], k["x"], k["a"], None)
+                got.append(block.leave(k["x"], k["y"], k["P"], k["b"], **how))
+                got += block.leave_enter(k["x"], k["y"], k["P"], k["b"], **how, **nxt)
+                got += block.leave_backward(k["D"], k["x"], k["y"], k["P"], k["b"], **how)
+                got += block.leave_enter_backward(k["D"], k["dh"], k["x"], k["x"], k["y"], k["P"], k["b"], **how, **nxt)
+        return got
+
+    plain = results()
+    monkeypatch.setattr(block, "_module", Nothing())
+    full = results()
+    assert len(plain) == len(full)
+    for p, q in zip(plain, full):
+        assert (p is None) == (q is None)
+        assert p is None or (p.dtype == q.dtype and torch.equal(p, q))
+
+
 def test_no_tokens():
     x, y, w = torch.empty(0, 4, 64, device=DEV), torch.empty(0, 64, device=DEV), rnd(1, 64)
     assert block.enter(x, None, w).shape == (0, 64)
