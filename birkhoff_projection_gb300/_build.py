@@ -27,7 +27,7 @@ BINDING_SOURCE = os.path.join(CSRC, "block_binding.cpp")
 SOURCES = ["birkhoff4_api.cu", "k_forward.cu", "k_backward.cu", "k_fused.cu", "k_sinkhorn.cu",
            "birkhoff4_noalloc.cu", "k_nxn.cu", "eot_stream.cu",
            "eot_transport.cu", "k_mapped.cu", "hcb_api.cu", "hcb_enter.cu", "hcb_leave.cu",
-           "hcb_leave_bwd.cu", "hcb_leave_enter_bwd.cu", "adamw.cu"]
+           "hcb_leave_bwd.cu", "hcb_leave_enter_bwd.cu", "hcb_residual.cu", "adamw.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "-I", CSRC, "-I", INCLUDE]

@@ -229,8 +229,11 @@ int hcb_leave_backward(const hcb_args* a, birkhoff4_stream_t stream) {
     p.wn.p = nullptr;
   }
   int rows = 0;
-  cudaError_t e = (next ? leave_enter_backward : leave_backward)(p, a->x_dtype == B4_BF16, a->y_dtype == B4_BF16,
-                                                                vectors(a, p), &rows, s);
+  const int xb = a->x_dtype == B4_BF16, yb = a->y_dtype == B4_BF16;
+  const bool vec = vectors(a, p);
+  cudaError_t e;
+  if (!residual_backward(p, xb, yb, vec, &rows, s, &e))
+    e = (next ? leave_enter_backward : leave_backward)(p, xb, yb, vec, &rows, s);
   if (e == cudaSuccess) e = finish(a, p, rows, s);
   return b4::record_cuda_error(e);
 }

@@ -7,10 +7,11 @@
 // token at a time; a CTA holds NG groups, and the grid is persistent (SMs x
 // resident CTAs).  A warp owns the same blocks of 32 V channels of every
 // token, k = 0 .. K - 1, where V elements are 16 bytes of the wider row type.
-// Where rows allow vectors, lane l has the V channels from l V on in a block;
-// where they do not (ODD), it has the pairs of channels 64 i + 2 l, so that a
-// warp's accesses of 4 bytes are to neighbouring words (with V channels to a
-// lane they were 16 bytes apart, and leave at 5001 x 4 x 1001 took 41 us).
+// Where rows allow vectors (ODD 0), lane l has the V channels from l V on in a
+// block; where they do not, a warp's accesses of 4 bytes are to neighbouring
+// words: it has the pairs of channels 64 i + 2 l (ODD 1), or, where all rows
+// are fp32, the channels 32 i + l (ODD 2).  (With V channels to a lane they
+// were 16 bytes apart, and leave at 5001 x 4 x 1001 took 41 us.)
 //
 // Loads.  All of these kernels are bound by memory, and a row's sums keep a
 // group waiting at a barrier; loads into registers then left the memory idle
@@ -40,6 +41,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include "b4_device.cuh"
 #include "b4_pairs.cuh"
@@ -93,7 +95,18 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <class T, int V, bool ODD>
+// Channel of a lane's element e in a block that begins at c (ODD 1 and 2).
+template <int ODD>
+__device__ __forceinline__ int channel(int c, int lane, int e) {
+  return ODD == 1 ? c + 64 * (e / 2) + 2 * lane + e % 2 : c + 32 * e + lane;
+}
+// Whether a block lies within its row, with one word behind it.
+template <int V>
+__device__ __forceinline__ bool inside(int c, int C) {
+  return c + 32 * V + 2 <= C;
+}
+
+template <class T, int V, int ODD>
 struct Row {
   static constexpr int H = V / 2;
   static constexpr int BYTES = V * static_cast<int>(sizeof(T));
@@ -105,9 +118,11 @@ struct Row {
   __device__ __forceinline__ static int straddles(const T* row, int c) {
     return SPLIT ? static_cast<int>(reinterpret_cast<uintptr_t>(row + c) & 2) : 0;
   }
-  // Begin the copy of the lane's elements into the slot at s.
+  // Begin the copy of the lane's elements into the slot at s.  FULL: the block
+  // is inside the row (any block where rows allow vectors).
+  template <bool FULL>
   __device__ __forceinline__ static void copy(char* s, int lane, const T* row, int c, int C) {
-    if constexpr (!ODD) {
+    if constexpr (ODD == 0) {
       const uint32_t d = b4::smem_addr(s + lane * BYTES);
       const T* p = row + min(c, C - V);
       if constexpr (BYTES == 16)
@@ -116,34 +131,30 @@ struct Row {
         copy8(d, p, c < C ? 8 : 0);
     } else if constexpr (SPLIT) {
       const int before = straddles(row, c);
-      const char* block = reinterpret_cast<const char*>(row + c) - before;
-      const char* valid = reinterpret_cast<const char*>(row) - straddles(row, 0);
-      const char* p = block + 4 * lane;
+      const char* p = reinterpret_cast<const char*>(row + c) - before + 4 * lane;
       const uint32_t d = b4::smem_addr(s + 4 * lane);
-      if (c + 32 * V + 2 <= C) {  // all of its words lie within the row
+      if constexpr (FULL) {
 #pragma unroll
         for (int i = 0; i < H; ++i) copy4(d + 128 * i, p + 128 * i);
-        if (before && lane == 31) copy4(d + 128 * (H - 1) + 4, p + 128 * (H - 1) + 4);
+        if (lane == 31) copy4(d + 128 * (H - 1) + 4, p + 128 * (H - 1) + 4);
       } else {
+        const char* valid = reinterpret_cast<const char*>(row) - straddles(row, 0);
         const int end = 2 * (C - c) + before - 4 * lane;  // bytes from p to the row's end
 #pragma unroll
         for (int i = 0; i < H; ++i) copy4_of(d + 128 * i, p + 128 * i, valid, end - 128 * i);
-        if (before && lane == 31)
-          copy4_of(d + 128 * (H - 1) + 4, p + 128 * (H - 1) + 4, valid, end - 128 * (H - 1) - 4);
+        if (lane == 31) copy4_of(d + 128 * (H - 1) + 4, p + 128 * (H - 1) + 4, valid, end - 128 * (H - 1) - 4);
       }
     } else {
-      const T* p = row + c + 2 * lane;
-      const uint32_t d = b4::smem_addr(s + 8 * lane);
-      if (c + 32 * V <= C && (reinterpret_cast<uintptr_t>(p) & 7) == 0) {
+      // four bytes to an element, in the order of the lane's elements: planes
+      // of pairs (ODD 1) or of words
 #pragma unroll
-        for (int i = 0; i < H; ++i) copy8(d + 256 * i, p + 64 * i);
-      } else {
-        const int end = 4 * (C - c - 2 * lane);
-#pragma unroll
-        for (int i = 0; i < H; ++i) {
-          copy4_of(d + 256 * i, p + 64 * i, row, end - 256 * i);
-          copy4_of(d + 256 * i + 4, p + 64 * i + 1, row, end - 256 * i - 4);
-        }
+      for (int e = 0; e < V; ++e) {
+        const int at = channel<ODD>(c, lane, e);
+        const uint32_t d = b4::smem_addr(s + (ODD == 1 ? 256 * (e / 2) + 8 * lane + 4 * (e % 2) : 128 * e + 4 * lane));
+        if constexpr (FULL)
+          copy4(d, row + at);
+        else
+          copy4_of(d, row + at, row, 4 * (C - at));
       }
     }
   }
@@ -153,6 +164,12 @@ struct Row {
     raw(s, lane, row, c, w);
     unpack(w, v);
   }
+  // The same as they are in memory, and their values.
+  __device__ __forceinline__ static void arrived_raw(const char* s, int lane, const T* row, int c,
+                                                     uint32_t (&w)[BYTES / 4]) {
+    raw(s, lane, row, c, w);
+  }
+  __device__ __forceinline__ static void values(const uint32_t (&w)[BYTES / 4], P2 (&v)[H]) { unpack(w, v); }
   // The same, and kept as they are at `to`.
   __device__ __forceinline__ static void arrived_kept(const char* s, int lane, const T* row, int c, P2 (&v)[H],
                                                       char* to) {
@@ -171,11 +188,11 @@ struct Row {
   }
   // The lane's elements read directly, zeros past C.
   __device__ __forceinline__ static void load(const T* row, int c, int lane, int C, P2 (&v)[H]) {
-    if constexpr (ODD) {
+    if constexpr (ODD != 0) {
 #pragma unroll
       for (int i = 0; i < H; ++i) {
-        const int e = c + 64 * i + 2 * lane;
-        v[i] = pair(e < C ? value(row + e) : 0.0f, e + 1 < C ? value(row + e + 1) : 0.0f);
+        const int a = channel<ODD>(c, lane, 2 * i), b = channel<ODD>(c, lane, 2 * i + 1);
+        v[i] = pair(a < C ? value(row + a) : 0.0f, b < C ? value(row + b) : 0.0f);
       }
     } else {
       uint32_t w[BYTES / 4];
@@ -206,19 +223,19 @@ struct Row {
   __device__ __forceinline__ static void raw(const char* s, int lane, const T* row, int c, uint32_t (&w)[BYTES / 4]) {
     if constexpr (SPLIT) {
       const uint32_t* q = reinterpret_cast<const uint32_t*>(s) + lane;
-      if (straddles(row, c)) {
+      const bool split = straddles(row, c) != 0;
+      const uint32_t which = split ? 0x5432 : 0x3210;
 #pragma unroll
-        for (int i = 0; i < H; ++i) w[i] = __byte_perm(q[32 * i], q[32 * i + 1], 0x5432);
-      } else {
-#pragma unroll
-        for (int i = 0; i < H; ++i) w[i] = q[32 * i];
-      }
-    } else if constexpr (ODD) {
+      for (int i = 0; i < H; ++i) w[i] = __byte_perm(q[32 * i], split ? q[32 * i + 1] : 0, which);
+    } else if constexpr (ODD == 1) {
 #pragma unroll
       for (int i = 0; i < H; ++i) {
         const uint2 q = *reinterpret_cast<const uint2*>(s + 256 * i + 8 * lane);
         w[(2 * i) % (BYTES / 4)] = q.x, w[(2 * i + 1) % (BYTES / 4)] = q.y;
       }
+    } else if constexpr (ODD == 2) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) w[e % (BYTES / 4)] = *reinterpret_cast<const uint32_t*>(s + 128 * e + 4 * lane);
     } else {
       words(s + lane * BYTES, w);
     }
@@ -250,7 +267,7 @@ struct Row {
     }
   }
   __device__ __forceinline__ static void put(T* row, int c, int lane, int C, const uint32_t (&w)[BYTES / 4]) {
-    if constexpr (!ODD) {
+    if constexpr (ODD == 0) {
       if (c >= C) return;
       if constexpr (BYTES == 16)
         *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -258,12 +275,11 @@ struct Row {
         *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
     } else if constexpr (SPLIT) {
       uint16_t* p = reinterpret_cast<uint16_t*>(row + c + 2 * lane);
-      const bool whole = c + 32 * V <= C;
-      if (whole && !straddles(row, c)) {
+      if (inside<V>(c, C) && !straddles(row, c)) {
 #pragma unroll
         for (int i = 0; i < H; ++i) reinterpret_cast<uint32_t*>(p)[32 * i] = w[i];
       } else {
-        const int left = whole ? 32 * V : C - c - 2 * lane;
+        const int left = C - c - 2 * lane;
 #pragma unroll
         for (int i = 0; i < H; ++i) {
           if (64 * i < left) p[64 * i] = static_cast<uint16_t>(w[i]);
@@ -271,18 +287,10 @@ struct Row {
         }
       }
     } else {
-      uint32_t* p = reinterpret_cast<uint32_t*>(row + c + 2 * lane);
-      if (c + 32 * V <= C && (reinterpret_cast<uintptr_t>(p) & 7) == 0) {
 #pragma unroll
-        for (int i = 0; i < H; ++i)
-          *reinterpret_cast<uint2*>(p + 64 * i) = make_uint2(w[(2 * i) % (BYTES / 4)], w[(2 * i + 1) % (BYTES / 4)]);
-      } else {
-        const int left = C - c - 2 * lane;
-#pragma unroll
-        for (int i = 0; i < H; ++i) {
-          if (64 * i < left) p[64 * i] = w[(2 * i) % (BYTES / 4)];
-          if (64 * i + 1 < left) p[64 * i + 1] = w[(2 * i + 1) % (BYTES / 4)];
-        }
+      for (int e = 0; e < V; ++e) {
+        const int at = channel<ODD>(c, lane, e);
+        if (at < C) reinterpret_cast<uint32_t*>(row)[at] = w[e % (BYTES / 4)];
       }
     }
   }
@@ -291,19 +299,19 @@ struct Row {
 // All of the thread's copies, or the oldest of DEPTH, have arrived; a slot has been read and may be
 // copied to again.  A lane of an ODD kernel reads a word of its neighbour's,
 // so there the warp waits for each other (all of its branches are the warp's).
-template <bool ODD>
+template <int ODD>
 __device__ __forceinline__ void slots_ready() {
   copy_wait_all();
-  if constexpr (ODD) __syncwarp();
+  if constexpr (ODD != 0) __syncwarp();
 }
-template <int DEPTH, bool ODD>
+template <int DEPTH, int ODD>
 __device__ __forceinline__ void slot_ready() {
   copy_wait<DEPTH - 1>();
-  if constexpr (ODD) __syncwarp();
+  if constexpr (ODD != 0) __syncwarp();
 }
-template <bool ODD>
+template <int ODD>
 __device__ __forceinline__ void slot_read() {
-  if constexpr (ODD) __syncwarp();
+  if constexpr (ODD != 0) __syncwarp();
 }
 
 // V floats that a thread keeps for itself, in its warp's planes of four.
@@ -322,23 +330,29 @@ __device__ __forceinline__ void kept(const char* s, int lane, P2 (&v)[V / 2]) {
 
 // A lane's elements of a row of partial weight gradients (whole vectors, see
 // pitch).
-template <int V, bool ODD>
+template <int V, int ODD>
 struct PartRow {
   __device__ __forceinline__ static void put(float* row, int c, int lane, int C, const P2 (&v)[V / 2]) {
-    if constexpr (ODD) {
+    if constexpr (ODD != 0) {
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i)
-        if (c + 64 * i + 2 * lane < C) *reinterpret_cast<P2*>(row + c + 64 * i + 2 * lane) = v[i];
+      for (int i = 0; i < V / 2; ++i) {
+        float lo, hi;
+        split(v[i], lo, hi);
+        if (channel<ODD>(c, lane, 2 * i) < C) row[channel<ODD>(c, lane, 2 * i)] = lo;
+        if (channel<ODD>(c, lane, 2 * i + 1) < C) row[channel<ODD>(c, lane, 2 * i + 1)] = hi;
+      }
     } else if (c < C) {
 #pragma unroll
       for (int i = 0; i < V / 4; ++i) put16(row + c + 4 * i, v[2 * i], v[2 * i + 1]);
     }
   }
   __device__ __forceinline__ static void get(const float* row, int c, int lane, int C, P2 (&v)[V / 2]) {
-    if constexpr (ODD) {
+    if constexpr (ODD != 0) {
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i)
-        v[i] = c + 64 * i + 2 * lane < C ? *reinterpret_cast<const P2*>(row + c + 64 * i + 2 * lane) : 0;
+      for (int i = 0; i < V / 2; ++i) {
+        const int a = channel<ODD>(c, lane, 2 * i), b = channel<ODD>(c, lane, 2 * i + 1);
+        v[i] = pair(a < C ? row[a] : 0.0f, b < C ? row[b] : 0.0f);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < V / 4; ++i) get16(row + min(c, C - V) + 4 * i, v[2 * i], v[2 * i + 1]);
@@ -349,7 +363,7 @@ struct PartRow {
 // Add a b to a thread's share of a weight gradient: in shared memory at s,
 // or, where rows are too long for that, in the group's row of the partial
 // sums (global memory that only this thread touches; such groups are CTAs).
-template <int V, bool ODD>
+template <int V, int ODD>
 __device__ __forceinline__ void add_share(char* s, float* row, int c, int lane, int C, const P2 (&a)[V / 2],
                                           const P2 (&b)[V / 2]) {
   P2 d[V / 2];
@@ -371,6 +385,9 @@ __device__ __forceinline__ void add_share(char* s, float* row, int c, int lane, 
 struct Any {
   const void* p;
   int32_t bf16;
+  __device__ __forceinline__ float at_far(int64_t i) const {
+    return bf16 ? b4::bf16lo(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
+  }
   __device__ __forceinline__ float at(int i) const {
     return bf16 ? b4::bf16lo(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
   }
@@ -378,20 +395,23 @@ struct Any {
   // of its values), 1 where there is none.  W says what is known of it: nothing (0), or that it is there, on
   // 16 bytes, and fp32 (1) or bf16 (2).  Told apart at run time, both types'
   // loads, conversions and choices between them are issued every time.
-  template <int V, bool ODD, int W>
+  template <int V, int ODD, int W>
   __device__ __forceinline__ void load(int c, int lane, int C, P2 (&v)[V / 2]) const {
     if (W == 0 && p == nullptr) {
 #pragma unroll
       for (int k = 0; k < V / 2; ++k) v[k] = twice(1.0f);
-    } else if constexpr (ODD) {
+    } else if constexpr (ODD != 0) {
 #pragma unroll
       for (int k = 0; k < V / 2; ++k) {
-        const int e = c + 64 * k + 2 * lane;
-        if (W == 1 && e + 1 < C) {
-          const float2 q = *reinterpret_cast<const float2*>(static_cast<const float*>(p) + e);
+        const int a = channel<ODD>(c, lane, 2 * k), b = channel<ODD>(c, lane, 2 * k + 1);
+        if (W == 1 && ODD == 1 && b < C) {
+          const float2 q = *reinterpret_cast<const float2*>(static_cast<const float*>(p) + a);
           v[k] = pair(q.x, q.y);
+        } else if constexpr (W == 1) {
+          const float* q = static_cast<const float*>(p);
+          v[k] = pair(a < C ? q[a] : 0.0f, b < C ? q[b] : 0.0f);
         } else {
-          v[k] = pair(e < C ? at(e) : 0.0f, W != 1 && e + 1 < C ? at(e + 1) : 0.0f);
+          v[k] = pair(a < C ? at(a) : 0.0f, b < C ? at(b) : 0.0f);
         }
       }
     } else if (W == 2 || (W == 0 && bf16)) {
@@ -452,9 +472,9 @@ __device__ __forceinline__ const T* at_row(const void* p, uint32_t t, uint32_t s
 
 // The channel that a thread of a group has in its first block (ODD: its
 // warp's first channel there).
-template <int V, bool ODD>
+template <int V, int ODD>
 __device__ __forceinline__ int first_channel(int l) {
-  return ODD ? l / 32 * 32 * V : l * V;
+  return ODD != 0 ? l / 32 * 32 * V : l * V;
 }
 
 // Floats of a row of partial weight gradients: whole vectors.
@@ -462,7 +482,7 @@ __host__ __device__ constexpr int pitch(int C) { return (C + 7) / 8 * 8; }
 
 // Write a CTA's sums of its NG groups' shares to its row (group 0's threads).
 // `first`: where the first item of this thread's warp is in group 0.
-template <int V, bool ODD>
+template <int V, int ODD>
 __device__ __forceinline__ void sum_shares(const char* first, const Params& p, int NG, int item, float* row) {
   if (threadIdx.x >= p.G) return;
   const int lane = threadIdx.x & 31;
@@ -779,6 +799,17 @@ cudaError_t launch(const Params& p, Shape sh, int max_grid, int* grid, cudaStrea
   return cudaGetLastError();
 }
 
+// Runs f(FULL) for a block of a row's copies: FULL (a true_type) where rows
+// allow vectors or the block is inside its row, so that all rows of an item
+// share one branch.
+template <int V, int ODD, class F>
+__device__ __forceinline__ void by_block(int c, int C, F&& f) {
+  if (ODD == 0 || inside<V>(c, C))
+    f(std::true_type());
+  else
+    f(std::false_type());
+}
+
 // Call F.operator()<SP, EXACT, TX, TY, V, ODD>() for the streams (SP of them:
 // 1, 2, 4 or 8; fewer, !EXACT, are rounded up, and the missing ones count as
 // zeros), the row types and alignment.  An EXACT kernel takes it further that
@@ -790,13 +821,13 @@ template <int SP, bool EXACT, class F>
 cudaError_t by_type(int x_bf16, int y_bf16, bool vec, F&& f) {
   constexpr int VB = SP == 8 ? 4 : 8;
   if (x_bf16)
-    return vec ? f.template operator()<SP, EXACT, bf16_t, bf16_t, VB, false>()
-               : f.template operator()<SP, EXACT, bf16_t, bf16_t, VB, true>();
+    return vec ? f.template operator()<SP, EXACT, bf16_t, bf16_t, VB, 0>()
+               : f.template operator()<SP, EXACT, bf16_t, bf16_t, VB, 1>();
   if (y_bf16)
-    return vec ? f.template operator()<SP, EXACT, float, bf16_t, 4, false>()
-               : f.template operator()<SP, EXACT, float, bf16_t, 4, true>();
-  return vec ? f.template operator()<SP, EXACT, float, float, 4, false>()
-             : f.template operator()<SP, EXACT, float, float, 4, true>();
+    return vec ? f.template operator()<SP, EXACT, float, bf16_t, 4, 0>()
+               : f.template operator()<SP, EXACT, float, bf16_t, 4, 1>();
+  return vec ? f.template operator()<SP, EXACT, float, float, 4, 0>()
+             : f.template operator()<SP, EXACT, float, float, 4, 2>();
 }
 template <class F>
 cudaError_t by_streams(int S, int x_bf16, int y_bf16, bool vec, F&& f) {
@@ -820,5 +851,8 @@ cudaError_t enter_backward(const Params& p, int x_bf16, int y_bf16, bool vec, in
 cudaError_t leave_forward(const Params& p, int x_bf16, int y_bf16, bool vec, cudaStream_t s);
 cudaError_t leave_backward(const Params& p, int x_bf16, int y_bf16, bool vec, int* rows, cudaStream_t s);
 cudaError_t leave_enter_backward(const Params& p, int x_bf16, int y_bf16, bool vec, int* rows, cudaStream_t s);
+// One stream without a mixing matrix, rows of one item to a thread
+// (hcb_residual.cu); false where a pass is not that.
+bool residual_backward(const Params& p, int x_bf16, int y_bf16, bool vec, int* rows, cudaStream_t s, cudaError_t* e);
 
 }  // namespace hcb

@@ -22,7 +22,7 @@ namespace hcb {
 
 // u = sum_s a_s x_s and its mean square in one pass over the row's streams;
 // u stays in shared memory (fp32) until r is known, then h = w u r.
-template <int SP, class TX, class TY, int V, bool ODD>
+template <int SP, class TX, class TY, int V, int ODD>
 struct Enter {
   using RX = Row<TX, V, ODD>;
   using RY = Row<TY, V, ODD>;
@@ -36,7 +36,7 @@ struct Enter {
   }
 };
 
-template <int SP, bool EXACT, class TX, class TY, int V, bool ODD, int W>
+template <int SP, bool EXACT, class TX, class TY, int V, int ODD, int W>
 __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
   using E = Enter<SP, TX, TY, V, ODD>;
   using RX = typename E::RX;
@@ -67,9 +67,12 @@ __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
   auto copy_next = [&] {
     slot_read<ODD>();
     if (ta < p.T && ca < C) {
+      by_block<V, ODD>(ca, C, [&](auto full) {
+        constexpr bool FULL = decltype(full)::value;
 #pragma unroll
-      for (int i = 0; i < SP; ++i)
-        if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, xa + i * p.x_ss, ca, C);
+        for (int i = 0; i < SP; ++i)
+          if (EXACT || i < S) RX::template copy<FULL>(slot_a + i * RX::SLOT, lane, xa + i * p.x_ss, ca, C);
+      });
     }
     copy_commit();
     ca += GV;
@@ -136,7 +139,7 @@ __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
 // <G, u> = sum a_s <G, x_s>, <u, u> = sum a_s <u, x_s> and
 // da_s = r (<G, x_s> - k <u, x_s>), so one pass over the row finds them and
 // a second, over what the first kept and over dres, writes.
-template <int SP, class TX, class TY, int V, bool ODD>
+template <int SP, class TX, class TY, int V, int ODD>
 struct EnterBackward {
   using RX = Row<TX, V, ODD>;
   using RY = Row<TY, V, ODD>;
@@ -152,7 +155,7 @@ struct EnterBackward {
   }
 };
 
-template <int SP, bool EXACT, class TX, class TY, int V, bool ODD, int W>
+template <int SP, bool EXACT, class TX, class TY, int V, int ODD, int W>
 __global__ void __launch_bounds__(256, SP == 8 ? 1 : HCB_ENTER_BWD_MINB) enter_backward_kernel(const Params p) {
   using E = EnterBackward<SP, TX, TY, V, ODD>;
   using RX = typename E::RX;
@@ -192,11 +195,13 @@ __global__ void __launch_bounds__(256, SP == 8 ? 1 : HCB_ENTER_BWD_MINB) enter_b
       const TX* x = second ? at_row<TX>(p.dres, ta, p.dres_ts)
                            : at_row<TX>(p.x, ta, p.x_ts);
       const int64_t ss = second ? p.dres_ss : p.x_ss;
+      by_block<V, ODD>(ca, C, [&](auto full) {
+        constexpr bool FULL = decltype(full)::value;
 #pragma unroll
-      for (int i = 0; i < SP; ++i)
-        if (EXACT || i < S) RX::copy(slot_a + i * RX::SLOT, lane, x + i * ss, ca, C);
-      if (!second)
-        RY::copy(slot_a + E::DH, lane, at_row<TY>(p.dh, ta, p.dh_ts), ca, C);
+        for (int i = 0; i < SP; ++i)
+          if (EXACT || i < S) RX::template copy<FULL>(slot_a + i * RX::SLOT, lane, x + i * ss, ca, C);
+        if (!second) RY::template copy<FULL>(slot_a + E::DH, lane, at_row<TY>(p.dh, ta, p.dh_ts), ca, C);
+      });
     }
     copy_commit();
     ca += GV;
@@ -332,14 +337,14 @@ namespace {
 struct Forward {
   const Params& p;
   cudaStream_t s;
-  template <int SP, bool EXACT, class TX, class TY, int V, bool ODD>
+  template <int SP, bool EXACT, class TX, class TY, int V, int ODD>
   cudaError_t operator()() const {
     Params q = p;
     int grid;
     const Shape sh = plan(q, shape_of(p.T, p.C, V, HCB_ENTER_PER, kMaxGroup), V, Enter<SP, TX, TY, V, ODD>::need);
     const int w = EXACT ? Weights::kind(p.w) : 0;
     if (w == 1) return launch<enter_kernel<SP, EXACT, TX, TY, V, ODD, EXACT ? 1 : 0>>(q, sh, 1 << 30, &grid, s);
-    if (w == 2 && !ODD) return launch<enter_kernel<SP, EXACT && !ODD, TX, TY, V, ODD, EXACT && !ODD ? 2 : 0>>(q, sh, 1 << 30, &grid, s);
+    if (w == 2 && ODD == 0) return launch<enter_kernel<SP, EXACT && ODD == 0, TX, TY, V, ODD, EXACT && ODD == 0 ? 2 : 0>>(q, sh, 1 << 30, &grid, s);
     return launch<enter_kernel<SP, false, TX, TY, V, ODD, 0>>(q, sh, 1 << 30, &grid, s);
   }
 };
@@ -347,7 +352,7 @@ struct Backward {
   const Params& p;
   int* rows;
   cudaStream_t s;
-  template <int SP, bool EXACT, class TX, class TY, int V, bool ODD>
+  template <int SP, bool EXACT, class TX, class TY, int V, int ODD>
   cudaError_t operator()() const {
     Params q = p;
     const Shape sh =
@@ -355,8 +360,8 @@ struct Backward {
     const int most = p.dw ? kMaxRows : 1 << 30;
     const int w = EXACT && !q.direct ? Weights::kind(p.w) : 0;
     if (w == 1) return launch<enter_backward_kernel<SP, EXACT, TX, TY, V, ODD, EXACT ? 1 : 0>>(q, sh, most, rows, s);
-    if (w == 2 && !ODD)
-      return launch<enter_backward_kernel<SP, EXACT && !ODD, TX, TY, V, ODD, EXACT && !ODD ? 2 : 0>>(q, sh, most, rows, s);
+    if (w == 2 && ODD == 0)
+      return launch<enter_backward_kernel<SP, EXACT && ODD == 0, TX, TY, V, ODD, EXACT && ODD == 0 ? 2 : 0>>(q, sh, most, rows, s);
     return launch<enter_backward_kernel<SP, false, TX, TY, V, ODD, 0>>(q, sh, most, rows, s);
   }
 };

@@ -12,14 +12,14 @@ namespace hcb {
 // The output's norm has to be known before the first stream is written, so a
 // token is two runs of items: y (and the gate), of which w act(gate) y is
 // kept in fp32 while its square is summed, then the streams.
-template <int SP, bool WHOLE, class TX, class TY, int V, bool ODD>
+template <int SP, bool WHOLE, class TX, class TY, int V, int ODD>
 struct Leave {
   using RX = Row<TX, V, ODD>;
   using RY = Row<TY, V, ODD>;
   using Co = Coefficients<SP, true, true, true>;
   using Sum = GroupSum<1>;
   // CTAs that the registers have to leave room for on an SM
-  static constexpr int MINB = SP <= 2 || (SP == 4 && V == 4 && !ODD) ? 3 : SP == 4 ? 2 : 1;
+  static constexpr int MINB = SP <= 2 || (SP == 4 && V == 4 && ODD == 0) ? 3 : SP == 4 ? 2 : 1;
   // a slot: the streams, or y and the gate; in one place only where both have
   // planes of one size, so that a lane's bytes are its own in both
   static constexpr int Y = RX::SLOT == RY::SLOT ? 0 : SP * RX::SLOT;
@@ -34,7 +34,7 @@ struct Leave {
 // copies the token's streams into the slots that it has read, and while it
 // works through those the next token's y, so that it only waits once a run.
 // Otherwise (rows too long for that) there is one slot, for the next item.
-template <int SP, bool EXACT, class TX, class TY, int V, bool ODD, int W>
+template <int SP, bool EXACT, class TX, class TY, int V, int ODD, int W>
 __global__ void __launch_bounds__(256, Leave<SP, EXACT, TX, TY, V, ODD>::MINB) leave_kernel(const Params p) {
   constexpr bool WHOLE = EXACT;
   using E = Leave<SP, WHOLE, TX, TY, V, ODD>;
@@ -63,14 +63,20 @@ __global__ void __launch_bounds__(256, Leave<SP, EXACT, TX, TY, V, ODD>::MINB) l
   uint32_t t = blockIdx.x * NG + group;
 
   auto copy_y = [&](uint32_t t, int c, char* slot) {
-    RY::copy(slot + E::Y, lane, at_row<TY>(p.y, t, p.y_ts), c, C);
-    if (gated) RY::copy(slot + E::Y + RY::SLOT, lane, at_row<TY>(p.gate, t, p.gate_ts), c, C);
+    by_block<V, ODD>(c, C, [&](auto full) {
+      constexpr bool FULL = decltype(full)::value;
+      RY::template copy<FULL>(slot + E::Y, lane, at_row<TY>(p.y, t, p.y_ts), c, C);
+      if (gated) RY::template copy<FULL>(slot + E::Y + RY::SLOT, lane, at_row<TY>(p.gate, t, p.gate_ts), c, C);
+    });
   };
   auto copy_x = [&](uint32_t t, int c, char* slot) {
     const TX* x = at_row<TX>(p.x, t, p.x_ts);
+    by_block<V, ODD>(c, C, [&](auto full) {
+      constexpr bool FULL = decltype(full)::value;
 #pragma unroll
-    for (int i = 0; i < SP; ++i)
-      if (EXACT || i < S) RX::copy(slot + i * RX::SLOT, lane, x + i * p.x_ss, c, C);
+      for (int i = 0; i < SP; ++i)
+        if (EXACT || i < S) RX::template copy<FULL>(slot + i * RX::SLOT, lane, x + i * p.x_ss, c, C);
+    });
   };
   Co co;
   co.init(p, lane);
@@ -215,18 +221,18 @@ namespace {
 struct Forward {
   const Params& p;
   cudaStream_t s;
-  template <int SP, bool EXACT, class TX, class TY, int V, bool ODD>
+  template <int SP, bool EXACT, class TX, class TY, int V, int ODD>
   cudaError_t operator()() const {
     Params q = p;
     int grid;
     const Shape want = shape_of(p.T, p.C, V, HCB_LEAVE_PER, 256);
     const int w = EXACT && (p.P.p != nullptr) == (SP > 1) ? Weights::kind(p.w, p.h ? p.wn : p.w) : 0;
-    if (w == 1 || (w == 2 && !ODD)) {
+    if (w == 1 || (w == 2 && ODD == 0)) {
       const Shape sh = plan(q, want, V, Leave<SP, true, TX, TY, V, ODD>::need);
       if (!q.direct && w == 1)
         return launch<leave_kernel<SP, EXACT, TX, TY, V, ODD, EXACT ? 1 : 0>>(q, sh, 1 << 30, &grid, s);
       if (!q.direct)
-        return launch<leave_kernel<SP, EXACT && !ODD, TX, TY, V, ODD, EXACT && !ODD ? 2 : 0>>(q, sh, 1 << 30, &grid, s);
+        return launch<leave_kernel<SP, EXACT && ODD == 0, TX, TY, V, ODD, EXACT && ODD == 0 ? 2 : 0>>(q, sh, 1 << 30, &grid, s);
     }
     const Shape sh = plan(q, want, V, Leave<SP, false, TX, TY, V, ODD>::need);
     return launch<leave_kernel<SP, false, TX, TY, V, ODD, 0>>(q, sh, 1 << 30, &grid, s);

@@ -26,7 +26,7 @@ namespace hcb {
 // writes dy, dgate and the weight's shares.
 // NEXT adds a run of items before it: D_i = dout_i + a_i du with du from dh,
 // as in enter_backward_kernel.
-template <int SP, class TX, class TY, int V, bool ODD, bool NEXT>
+template <int SP, class TX, class TY, int V, int ODD, bool NEXT>
 struct LeaveBackward {
   using RX = Row<TX, V, ODD>;
   using RY = Row<TY, V, ODD>;
@@ -53,7 +53,7 @@ struct LeaveBackward {
 };
 
 // GATE: 0 no gate, 1 a gate, 2 told at run time.
-template <int SP, bool EXACT, class TX, class TY, int V, bool ODD, bool NEXT, int GATE, int W>
+template <int SP, bool EXACT, class TX, class TY, int V, int ODD, bool NEXT, int GATE, int W>
 __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::minb(GATE)) leave_backward_kernel(const Params p) {
   using E = LeaveBackward<SP, TX, TY, V, ODD, NEXT>;
   using RX = typename E::RX;
@@ -96,18 +96,21 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
     first = NEXT && first;
     const TX* d = first ? at_row<TX>(p.out_in, t, p.out_ts) : at_row<TX>(p.dout, t, p.dout_ts);
     const uint32_t ss = first ? p.out_ss : p.dout_ss;
-#pragma unroll
-    for (int i = 0; i < SP; ++i)
-      if (EXACT || i < S) RX::copy(slot + i * RX::SLOT, lane, d + i * ss, c, C);
-    RY::copy(slot + E::Y, lane, first ? at_row<TY>(p.dh, t, p.dh_ts) : at_row<TY>(p.y, t, p.y_ts), c, C);
-    if (first) return;
-    if (gated) RY::copy(slot + E::GATE, lane, at_row<TY>(p.gate, t, p.gate_ts), c, C);
-    if (mix) {
-      const TX* x = at_row<TX>(p.x, t, p.x_ts);
+    by_block<V, ODD>(c, C, [&](auto full) {
+      constexpr bool FULL = decltype(full)::value;
 #pragma unroll
       for (int i = 0; i < SP; ++i)
-        if (EXACT || i < S) RX::copy(slot + E::X + i * RX::SLOT, lane, x + i * p.x_ss, c, C);
-    }
+        if (EXACT || i < S) RX::template copy<FULL>(slot + i * RX::SLOT, lane, d + i * ss, c, C);
+      RY::template copy<FULL>(slot + E::Y, lane, first ? at_row<TY>(p.dh, t, p.dh_ts) : at_row<TY>(p.y, t, p.y_ts), c, C);
+      if (first) return;
+      if (gated) RY::template copy<FULL>(slot + E::GATE, lane, at_row<TY>(p.gate, t, p.gate_ts), c, C);
+      if (mix) {
+        const TX* x = at_row<TX>(p.x, t, p.x_ts);
+#pragma unroll
+        for (int i = 0; i < SP; ++i)
+          if (EXACT || i < S) RX::template copy<FULL>(slot + E::X + i * RX::SLOT, lane, x + i * p.x_ss, c, C);
+      }
+    });
   };
   Co co;
   co.init(p, lane);
@@ -398,7 +401,7 @@ struct Backward {
   const Params& p;
   int* rows;
   cudaStream_t s;
-  template <int SP, bool EXACT, class TX, class TY, int V, bool ODD>
+  template <int SP, bool EXACT, class TX, class TY, int V, int ODD>
   cudaError_t operator()() const {
     using E = LeaveBackward<SP, TX, TY, V, ODD, NEXT>;
     Params q = p;
@@ -417,7 +420,7 @@ struct Backward {
     Shape sh = plan(q, want, V, need(w != 0 && SP <= HCB_LEAVE_BWD_WHOLE));
     if (w != 0 && q.direct) w = 0;
     if (w == 0) sh = plan(q, want, V, need(false));
-    constexpr int W1 = EXACT ? 1 : 0, W2 = EXACT && !ODD ? 2 : 0;
+    constexpr int W1 = EXACT ? 1 : 0, W2 = EXACT && ODD == 0 ? 2 : 0;
     if (w == 1 && gated)
       return launch<leave_backward_kernel<SP, EXACT, TX, TY, V, ODD, NEXT, W1 ? 1 : 2, W1>>(q, sh, most, rows, s);
     if (w == 1)
