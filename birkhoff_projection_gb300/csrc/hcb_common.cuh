@@ -74,19 +74,33 @@ constexpr int kMaxRows = 640;   // CTAs of a backward pass at most (rows of part
 // word and the lower half of the next; past the row's last element nothing is
 // read (the copy's source size), and the slot holds zeros.
 // ---------------------------------------------------------------------------
+// Copies to shared memory, D and S bytes behind d and p: constants of the
+// instruction, not additions to an address.  n < the size: the rest are zeros;
+// nothing is read for n <= 0, wherever p points.
+template <int D, int S>
 __device__ __forceinline__ void copy4(uint32_t d, const void* p) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(p) : "memory");
+  asm volatile("cp.async.ca.shared.global [%0+%2], [%1+%3], 4;" ::"r"(d), "l"(p), "n"(D), "n"(S) : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t d, const void* p, int n = 8) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(p), "r"(n) : "memory");
+template <int D, int S>
+__device__ __forceinline__ void copy4_of(uint32_t d, const void* p, int n) {
+  asm volatile("cp.async.ca.shared.global [%0+%3], [%1+%4], 4, %2;" ::"r"(d), "l"(p), "r"(max(0, min(4, n))), "n"(D), "n"(S)
+               : "memory");
 }
-__device__ __forceinline__ void copy16(uint32_t d, const void* p, int n = 16) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(p), "r"(n) : "memory");
+template <int D>
+__device__ __forceinline__ void copy8(uint32_t d, const void* p, int n) {
+  asm volatile("cp.async.ca.shared.global [%0+%3], [%1], 8, %2;" ::"r"(d), "l"(p), "r"(n), "n"(D) : "memory");
 }
-// n of 4 bytes, the rest zero; p is not read if n <= 0 but has to be valid
-__device__ __forceinline__ void copy4_of(uint32_t d, const void* p, const void* valid, int n) {
-  n = max(0, min(4, n));
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(n > 0 ? p : valid), "r"(n) : "memory");
+template <int D>
+__device__ __forceinline__ void copy16(uint32_t d, const void* p, int n) {
+  asm volatile("cp.async.cg.shared.global [%0+%3], [%1], 16, %2;" ::"r"(d), "l"(p), "r"(n), "n"(D) : "memory");
+}
+// f(0), ... f(N - 1), each with its number as a constant.
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void each(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>());
+    each<N, I + 1>(f);
+  }
 }
 __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -118,44 +132,44 @@ struct Row {
   __device__ __forceinline__ static int straddles(const T* row, int c) {
     return SPLIT ? static_cast<int>(reinterpret_cast<uintptr_t>(row + c) & 2) : 0;
   }
-  // Begin the copy of the lane's elements into the slot at s.  FULL: the block
-  // is inside the row (any block where rows allow vectors).
-  template <bool FULL>
-  __device__ __forceinline__ static void copy(char* s, int lane, const T* row, int c, int C) {
+  // Begin the copy of the lane's elements into the slot `OFF` bytes behind s
+  // (the shared address of an item's slots).  FULL: the block is inside the
+  // row (any block where rows allow vectors).
+  template <bool FULL, int OFF>
+  __device__ __forceinline__ static void copy(uint32_t s, int lane, const T* row, int c, int C) {
     if constexpr (ODD == 0) {
-      const uint32_t d = b4::smem_addr(s + lane * BYTES);
       const T* p = row + min(c, C - V);
       if constexpr (BYTES == 16)
-        copy16(d, p, c < C ? 16 : 0);
+        copy16<OFF>(s + lane * 16, p, c < C ? 16 : 0);
       else
-        copy8(d, p, c < C ? 8 : 0);
+        copy8<OFF>(s + lane * 8, p, c < C ? 8 : 0);
     } else if constexpr (SPLIT) {
       const int before = straddles(row, c);
       const char* p = reinterpret_cast<const char*>(row + c) - before + 4 * lane;
-      const uint32_t d = b4::smem_addr(s + 4 * lane);
+      const uint32_t to = s + 4 * lane;
+      constexpr int LAST = 128 * (H - 1) + 4;
       if constexpr (FULL) {
-#pragma unroll
-        for (int i = 0; i < H; ++i) copy4(d + 128 * i, p + 128 * i);
-        if (lane == 31) copy4(d + 128 * (H - 1) + 4, p + 128 * (H - 1) + 4);
+        each<H>([&](auto i) { copy4<OFF + 128 * i.value, 128 * i.value>(to, p); });
+        if (lane == 31) copy4<OFF + LAST, LAST>(to, p);
       } else {
-        const char* valid = reinterpret_cast<const char*>(row) - straddles(row, 0);
         const int end = 2 * (C - c) + before - 4 * lane;  // bytes from p to the row's end
-#pragma unroll
-        for (int i = 0; i < H; ++i) copy4_of(d + 128 * i, p + 128 * i, valid, end - 128 * i);
-        if (lane == 31) copy4_of(d + 128 * (H - 1) + 4, p + 128 * (H - 1) + 4, valid, end - 128 * (H - 1) - 4);
+        each<H>([&](auto i) { copy4_of<OFF + 128 * i.value, 128 * i.value>(to, p, end - 128 * i.value); });
+        if (lane == 31) copy4_of<OFF + LAST, LAST>(to, p, end - LAST);
       }
     } else {
       // four bytes to an element, in the order of the lane's elements: planes
       // of pairs (ODD 1) or of words
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const int at = channel<ODD>(c, lane, e);
-        const uint32_t d = b4::smem_addr(s + (ODD == 1 ? 256 * (e / 2) + 8 * lane + 4 * (e % 2) : 128 * e + 4 * lane));
+      const T* p = row + channel<ODD>(c, lane, 0);
+      const uint32_t to = s + (ODD == 1 ? 8 : 4) * lane;
+      const int left = 4 * (C - channel<ODD>(c, lane, 0));
+      each<V>([&](auto e) {
+        constexpr int E = e.value, TO = OFF + (ODD == 1 ? 256 * (E / 2) + 4 * (E % 2) : 128 * E);
+        constexpr int FROM = ODD == 1 ? 256 * (E / 2) + 4 * (E % 2) : 128 * E;
         if constexpr (FULL)
-          copy4(d, row + at);
+          copy4<TO, FROM>(to, p);
         else
-          copy4_of(d, row + at, row, 4 * (C - at));
-      }
+          copy4_of<TO, FROM>(to, p, left - FROM);
+      });
     }
   }
   // The arrived slot's elements.
@@ -404,12 +418,9 @@ struct Any {
 #pragma unroll
       for (int k = 0; k < V / 2; ++k) {
         const int a = channel<ODD>(c, lane, 2 * k), b = channel<ODD>(c, lane, 2 * k + 1);
-        if (W == 1 && ODD == 1 && b < C) {
-          const float2 q = *reinterpret_cast<const float2*>(static_cast<const float*>(p) + a);
-          v[k] = pair(q.x, q.y);
-        } else if constexpr (W == 1) {
+        if constexpr (W == 1) {  // the nearest of its values where there is none
           const float* q = static_cast<const float*>(p);
-          v[k] = pair(a < C ? q[a] : 0.0f, b < C ? q[b] : 0.0f);
+          v[k] = pair(q[min(a, C - 1)], q[min(b, C - 1)]);
         } else {
           v[k] = pair(a < C ? at(a) : 0.0f, b < C ? at(b) : 0.0f);
         }

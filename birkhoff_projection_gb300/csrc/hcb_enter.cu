@@ -67,11 +67,13 @@ __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
   auto copy_next = [&] {
     slot_read<ODD>();
     if (ta < p.T && ca < C) {
+      const uint32_t to = b4::smem_addr(slot_a);
       by_block<V, ODD>(ca, C, [&](auto full) {
         constexpr bool FULL = decltype(full)::value;
-#pragma unroll
-        for (int i = 0; i < SP; ++i)
-          if (EXACT || i < S) RX::template copy<FULL>(slot_a + i * RX::SLOT, lane, xa + i * p.x_ss, ca, C);
+        each<SP>([&](auto i) {
+          if (EXACT || i.value < S)
+            RX::template copy<FULL, i.value * RX::SLOT>(to, lane, xa + i.value * p.x_ss, ca, C);
+        });
       });
     }
     copy_commit();
@@ -195,12 +197,13 @@ __global__ void __launch_bounds__(256, SP == 8 ? 1 : HCB_ENTER_BWD_MINB) enter_b
       const TX* x = second ? at_row<TX>(p.dres, ta, p.dres_ts)
                            : at_row<TX>(p.x, ta, p.x_ts);
       const int64_t ss = second ? p.dres_ss : p.x_ss;
+      const uint32_t to = b4::smem_addr(slot_a);
       by_block<V, ODD>(ca, C, [&](auto full) {
         constexpr bool FULL = decltype(full)::value;
-#pragma unroll
-        for (int i = 0; i < SP; ++i)
-          if (EXACT || i < S) RX::template copy<FULL>(slot_a + i * RX::SLOT, lane, x + i * ss, ca, C);
-        if (!second) RY::template copy<FULL>(slot_a + E::DH, lane, at_row<TY>(p.dh, ta, p.dh_ts), ca, C);
+        each<SP>([&](auto i) {
+          if (EXACT || i.value < S) RX::template copy<FULL, i.value * RX::SLOT>(to, lane, x + i.value * ss, ca, C);
+        });
+        if (!second) RY::template copy<FULL, E::DH>(to, lane, at_row<TY>(p.dh, ta, p.dh_ts), ca, C);
       });
     }
     copy_commit();

@@ -63,19 +63,21 @@ __global__ void __launch_bounds__(256, Leave<SP, EXACT, TX, TY, V, ODD>::MINB) l
   uint32_t t = blockIdx.x * NG + group;
 
   auto copy_y = [&](uint32_t t, int c, char* slot) {
+    const uint32_t to = b4::smem_addr(slot);
     by_block<V, ODD>(c, C, [&](auto full) {
       constexpr bool FULL = decltype(full)::value;
-      RY::template copy<FULL>(slot + E::Y, lane, at_row<TY>(p.y, t, p.y_ts), c, C);
-      if (gated) RY::template copy<FULL>(slot + E::Y + RY::SLOT, lane, at_row<TY>(p.gate, t, p.gate_ts), c, C);
+      RY::template copy<FULL, E::Y>(to, lane, at_row<TY>(p.y, t, p.y_ts), c, C);
+      if (gated) RY::template copy<FULL, E::Y + RY::SLOT>(to, lane, at_row<TY>(p.gate, t, p.gate_ts), c, C);
     });
   };
   auto copy_x = [&](uint32_t t, int c, char* slot) {
     const TX* x = at_row<TX>(p.x, t, p.x_ts);
+    const uint32_t to = b4::smem_addr(slot);
     by_block<V, ODD>(c, C, [&](auto full) {
       constexpr bool FULL = decltype(full)::value;
-#pragma unroll
-      for (int i = 0; i < SP; ++i)
-        if (EXACT || i < S) RX::template copy<FULL>(slot + i * RX::SLOT, lane, x + i * p.x_ss, c, C);
+      each<SP>([&](auto i) {
+        if (EXACT || i.value < S) RX::template copy<FULL, i.value * RX::SLOT>(to, lane, x + i.value * p.x_ss, c, C);
+      });
     });
   };
   Co co;

@@ -96,19 +96,21 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
     first = NEXT && first;
     const TX* d = first ? at_row<TX>(p.out_in, t, p.out_ts) : at_row<TX>(p.dout, t, p.dout_ts);
     const uint32_t ss = first ? p.out_ss : p.dout_ss;
+    const uint32_t to = b4::smem_addr(slot);
     by_block<V, ODD>(c, C, [&](auto full) {
       constexpr bool FULL = decltype(full)::value;
-#pragma unroll
-      for (int i = 0; i < SP; ++i)
-        if (EXACT || i < S) RX::template copy<FULL>(slot + i * RX::SLOT, lane, d + i * ss, c, C);
-      RY::template copy<FULL>(slot + E::Y, lane, first ? at_row<TY>(p.dh, t, p.dh_ts) : at_row<TY>(p.y, t, p.y_ts), c, C);
+      each<SP>([&](auto i) {
+        if (EXACT || i.value < S) RX::template copy<FULL, i.value * RX::SLOT>(to, lane, d + i.value * ss, c, C);
+      });
+      RY::template copy<FULL, E::Y>(to, lane, first ? at_row<TY>(p.dh, t, p.dh_ts) : at_row<TY>(p.y, t, p.y_ts), c, C);
       if (first) return;
-      if (gated) RY::template copy<FULL>(slot + E::GATE, lane, at_row<TY>(p.gate, t, p.gate_ts), c, C);
+      if (gated) RY::template copy<FULL, E::GATE>(to, lane, at_row<TY>(p.gate, t, p.gate_ts), c, C);
       if (mix) {
         const TX* x = at_row<TX>(p.x, t, p.x_ts);
-#pragma unroll
-        for (int i = 0; i < SP; ++i)
-          if (EXACT || i < S) RX::template copy<FULL>(slot + E::X + i * RX::SLOT, lane, x + i * p.x_ss, c, C);
+        each<SP>([&](auto i) {
+          if (EXACT || i.value < S)
+            RX::template copy<FULL, E::X + i.value * RX::SLOT>(to, lane, x + i.value * p.x_ss, c, C);
+        });
       }
     });
   };

@@ -49,18 +49,20 @@ __global__ void __launch_bounds__(kMaxGroup, 1) residual_backward_kernel(const P
   const uint32_t step = gridDim.x * NG;
 
   auto copy_next = [&](uint32_t t, char* slot) {
+    const uint32_t to = b4::smem_addr(slot);
     by_block<V, ODD>(c, C, [&](auto full) {
       constexpr bool FULL = decltype(full)::value;
-      RX::template copy<FULL>(slot, lane, at_row<TX>(p.out_in, t, p.out_ts), c, C);
-      RY::template copy<FULL>(slot + E::DH, lane, at_row<TY>(p.dh, t, p.dh_ts), c, C);
+      RX::template copy<FULL, 0>(to, lane, at_row<TX>(p.out_in, t, p.out_ts), c, C);
+      RY::template copy<FULL, E::DH>(to, lane, at_row<TY>(p.dh, t, p.dh_ts), c, C);
     });
   };
   auto copy_rest = [&](uint32_t t, char* slot) {
+    const uint32_t to = b4::smem_addr(slot);
     by_block<V, ODD>(c, C, [&](auto full) {
       constexpr bool FULL = decltype(full)::value;
-      RX::template copy<FULL>(slot + E::REST, lane, at_row<TX>(p.dout, t, p.dout_ts), c, C);
-      RY::template copy<FULL>(slot + E::Y, lane, at_row<TY>(p.y, t, p.y_ts), c, C);
-      if (GATED) RY::template copy<FULL>(slot + E::GATE, lane, at_row<TY>(p.gate, t, p.gate_ts), c, C);
+      RX::template copy<FULL, E::REST>(to, lane, at_row<TX>(p.dout, t, p.dout_ts), c, C);
+      RY::template copy<FULL, E::Y>(to, lane, at_row<TY>(p.y, t, p.y_ts), c, C);
+      if (GATED) RY::template copy<FULL, E::GATE>(to, lane, at_row<TY>(p.gate, t, p.gate_ts), c, C);
     });
   };
   uint32_t t0 = blockIdx.x * NG + group;
