@@ -38,7 +38,9 @@ class AdamW(torch.optim.Optimizer):
     master_weights: keep an fp32 copy of bf16 parameters and step on that.
     step(grad_scale=t) multiplies every gradient by the fp32 device scalar t.
     A parameter without a gradient is left alone, and so are its moments; all
-    parameters share one count of steps (the attribute `steps`)."""
+    parameters share one count of steps (the attribute `steps`).  The count and
+    the group's numbers are arguments of the launch: a step captured into a CUDA
+    graph repeats that very step."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 1e-2, *,
                  state_bits: int = 32, master_weights: bool = False):

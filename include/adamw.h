@@ -8,8 +8,9 @@
  *        - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
  *
  * Arithmetic is fp32; beta, 1 - beta and the step's other factors are worked
- * out in fp64 and rounded once.  The moments' updates round every product and sum by
- * itself (no fused multiply-add), so they can be reproduced bit for bit.
+ * out in fp64 and rounded once.  The moments' updates round every product
+ * and sum by itself (no fused multiply-add), so they can be reproduced bit for
+ * bit.
  *
  * Weights p and gradients g are B4_F32 or B4_BF16.  With `master` given the
  * step is taken on fp32 master weights, and p (bf16) is their rounded copy;
@@ -20,10 +21,11 @@
  * the root sqrt(v) of the second, which has half of v's range of exponents.
  * A block's scale is the largest finite magnitude in it times the fp32 number
  * 1/448 (448 is e4m3's largest), and a code is the nearest e4m3 number to
- * value * (448 * (1 / largest)), ties to even, every operation rounded.  sqrt(v) > 0 never becomes 0: it is at least e4m3's
- * smallest number, so that a denominator does not vanish under a first
- * moment that is kept.  A value that is not finite is stored as e4m3's NaN
- * and leaves the others of its block alone.
+ * value * (448 * (1 / largest)), ties to even, every operation rounded.
+ * sqrt(v) > 0 never becomes 0: it is at least e4m3's smallest number, so that
+ * a denominator does not vanish under a first moment that is kept.  A value
+ * that is not finite is stored as e4m3's NaN and leaves the others of its
+ * block alone.
  *
  * Layout: every tensor is n contiguous elements.  Any alignment of the
  * element type is taken; tensors on 16-byte boundaries are fastest.
@@ -35,7 +37,8 @@
  * B4_ENOTIMPL for master weights beside fp32 weights; B4_ECUDA for a launch
  * error.  Everything is checked before the first launch.  Work is
  * asynchronous on `stream`; the tables of pointers travel in the launches'
- * own arguments, so a captured step replays on the same tensors.
+ * own arguments, so a captured step replays on the same tensors, and with the
+ * same number of the step and learning rate.
  */
 #ifndef ADAMW_H
 #define ADAMW_H

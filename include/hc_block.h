@@ -47,9 +47,10 @@
  * Errors (return values, from birkhoff4.h): B4_EINVAL for a NULL pointer with
  * work to do, T outside 0..2^31 - 1, S outside 1..8, C outside
  * 1..HCB_MAX_CHANNELS, a negative or non-finite eps, a non-finite scale, a
- * stride outside 0..2^29 - 1, an unknown type or act, a pointer that is not aligned to its element, or a
- * workspace that is too small or not 16-byte aligned; B4_ENOTIMPL for x
- * B4_BF16 with y B4_F32; B4_ECUDA for a launch error.  T == 0 writes zeros to
+ * stride outside 0..2^29 - 1, an unknown type or act, a pointer that is not
+ * aligned to its element, or a workspace that is too small or not 16-byte
+ * aligned; B4_ENOTIMPL for x B4_BF16 with y B4_F32; B4_ECUDA for a launch
+ * error.  T == 0 writes zeros to
  * dw and dw_next and does nothing else.  Work is asynchronous on `stream`;
  * the library allocates nothing.  Outputs may not overlap the inputs, but
  * dx may be dres or dout (same strides), and dy may be y.
