@@ -102,6 +102,9 @@ __device__ __forceinline__ void each(F&& f) {
     each<N, I + 1>(f);
   }
 }
+// The next launch of the stream may be set up now, if it waits by itself for
+// this one's results (the sums of the partial weight gradients do).
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>

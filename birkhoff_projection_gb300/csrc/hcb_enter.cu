@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(256, SP == 8 ? 1 : HCB_ENTER_BWD_MINB) enter_b
   float* co_s = co_all + warp * Co::FLOATS;
   float* red = co_all + G / 32 * Co::FLOATS;
   Sum::clear(red, G, l);
+  let_next_launch();
   group_sync(G, group);
   float* row_dw = direct && p.dw ? p.dw + int64_t(blockIdx.x) * pitch(C) : nullptr;
   int turn = 0;

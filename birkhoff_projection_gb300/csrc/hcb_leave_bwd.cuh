@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
   float* red_next = red + Sum::floats(G);
   Sum::clear(red, G, l);
   if constexpr (NEXT) E::SumNext::clear(red_next, G, l);
+  let_next_launch();
   group_sync(G, group);
   float* row_dw = direct && p.dw ? p.dw + int64_t(blockIdx.x) * pitch(C) : nullptr;
   float* row_dwn = NEXT && direct && p.dwn ? p.dwn + int64_t(blockIdx.x) * pitch(C) : nullptr;

@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) residual_backward_kernel(const P
   float* red_next = red + Sum::floats(G);
   Sum::clear(red, G, l);
   if constexpr (NEXT) Sum::clear(red_next, G, l);
+  let_next_launch();
   group_sync(G, group);
   int turn = 0, turn_next = 0;
   const float inv_c = 1.0f / static_cast<float>(C);
