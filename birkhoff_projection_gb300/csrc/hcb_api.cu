@@ -209,8 +209,12 @@ int hcb_leave(const hcb_args* a, birkhoff4_stream_t stream) {
   Params p = params_of(a);
   p.x = a->x, p.y = a->y, p.gate = a->gate, p.out = a->out, p.h = a->h;
   if (a->h == nullptr) p.wn.p = nullptr;
-  return b4::record_cuda_error(leave_forward(p, a->x_dtype == B4_BF16, a->y_dtype == B4_BF16,
-                                             vectors(a, p), reinterpret_cast<cudaStream_t>(stream)));
+  const int xb = a->x_dtype == B4_BF16, yb = a->y_dtype == B4_BF16;
+  const bool vec = vectors(a, p);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (!residual_forward(p, xb, yb, vec, s, &e)) e = leave_forward(p, xb, yb, vec, s);
+  return b4::record_cuda_error(e);
 }
 
 int hcb_leave_backward(const hcb_args* a, birkhoff4_stream_t stream) {

@@ -867,6 +867,7 @@ cudaError_t leave_backward(const Params& p, int x_bf16, int y_bf16, bool vec, in
 cudaError_t leave_enter_backward(const Params& p, int x_bf16, int y_bf16, bool vec, int* rows, cudaStream_t s);
 // One stream without a mixing matrix, rows of one item to a thread
 // (hcb_residual.cu); false where a pass is not that.
+bool residual_forward(const Params& p, int x_bf16, int y_bf16, bool vec, cudaStream_t s, cudaError_t* e);
 bool residual_backward(const Params& p, int x_bf16, int y_bf16, bool vec, int* rows, cudaStream_t s, cudaError_t* e);
 
 }  // namespace hcb

@@ -1,4 +1,4 @@
-// hcb_residual.cu -- the gradient of leave and leave_enter for one stream
+// hcb_residual.cu -- leave and leave_enter and their gradients for one stream
 // without a mixing matrix (the residual of an ordinary network), where a row
 // is no longer than one vector to each of 512 threads.
 //
@@ -232,7 +232,166 @@ __global__ void __launch_bounds__(kMaxGroup, 1) residual_backward_kernel(const P
   if (NEXT && p.dwn) PartRow<V, ODD>::put(p.dwn + row, c, lane, C, dwn);
 }
 
+// leave and leave_enter likewise: the row, w act y and the result stay in
+// registers between the sums.  leave_enter at 16384 x 4096 bf16, tokens at a
+// time x CTAs on an SM: 1x2 103 us, 2x1 95, 2x2 105 (spilt), 3x1 86, 4x1 82.6
+// (6.5 TB/s, 96% of the copy's rate; 117 through shared memory in
+// hcb_leave.cu); fp32 vectors are half as many channels to a thread: 8192 x
+// 2048 with bf16 y and a gate 2x2 42 us, 4x1 44, 2x1 50.  Odd rows with bf16
+// ones among them are bound by their copies of single words and gain nothing
+// (4001 x 4001 bf16 44 us there, 50 here; 4096 x 1431 fp32 27 and 22.6).
+template <class TX, class TY, int V, int ODD, bool GATED>
+struct ResidualForward {
+  using RX = Row<TX, V, ODD>;
+  using RY = Row<TY, V, ODD>;
+  // tokens at a time, and CTAs that the registers have to leave room for
+  static constexpr int TOKENS = V == 8 ? 4 : 2, MINB = V == 8 ? 1 : 2;
+  using Sum = GroupSum<TOKENS>;
+  static constexpr int Y = RX::SLOT, GATE = Y + RY::SLOT, SLOT = GATED ? GATE + RY::SLOT : GATE;
+};
+
+template <class TX, class TY, int V, int ODD, bool NEXT, bool GATED, int W>
+__global__ void __launch_bounds__(kMaxGroup, ResidualForward<TX, TY, V, ODD, GATED>::MINB) residual_kernel(const Params p) {
+  using E = ResidualForward<TX, TY, V, ODD, GATED>;
+  using RX = typename E::RX;
+  using RY = typename E::RY;
+  using Sum = typename E::Sum;
+  constexpr int H = V / 2, N = E::TOKENS, SLOT = E::SLOT;
+  extern __shared__ __align__(16) char smem[];
+  const int G = p.G, NG = blockDim.x / G, group = threadIdx.x / G, l = threadIdx.x % G;
+  const int lane = threadIdx.x & 31, warp = l / 32, C = p.C, c = first_channel<V, ODD>(l);
+  char* of_group = smem + group * p.group_bytes;
+  char* ring = of_group + warp * p.warp_bytes;
+  float* red = reinterpret_cast<float*>(of_group + G / 32 * p.warp_bytes);
+  float* red_next = red + Sum::floats(G);
+  Sum::clear(red, G, l);
+  if constexpr (NEXT) Sum::clear(red_next, G, l);
+  group_sync(G, group);
+  int turn = 0, turn_next = 0;
+  const float inv_c = 1.0f / static_cast<float>(C);
+  const uint32_t step = gridDim.x * NG;
+
+  auto copy = [&](uint32_t t, char* slot) {
+    const uint32_t to = b4::smem_addr(slot);
+    by_block<V, ODD>(c, C, [&](auto full) {
+      constexpr bool FULL = decltype(full)::value;
+      RX::template copy<FULL, 0>(to, lane, at_row<TX>(p.x, t, p.x_ts), c, C);
+      RY::template copy<FULL, E::Y>(to, lane, at_row<TY>(p.y, t, p.y_ts), c, C);
+      if (GATED) RY::template copy<FULL, E::GATE>(to, lane, at_row<TY>(p.gate, t, p.gate_ts), c, C);
+    });
+  };
+  uint32_t t0 = blockIdx.x * NG + group;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const uint32_t t = t0 + n * step;
+    if (t < p.T) copy(t, ring + n * SLOT);
+  }
+  P2 w[H], wn[H];
+  p.w.load<V, ODD, W>(c, lane, C, w);
+  if (NEXT) p.wn.load<V, ODD, W>(c, lane, C, wn);
+
+#pragma unroll 1
+  for (; t0 < p.T; t0 += N * step) {
+    slots_ready<ODD>();
+    uint32_t x_raw[N][RX::BYTES / 4];
+    P2 v[N][H];
+    float a[N], b[N], sum[N], total[1];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const uint32_t t = t0 + n * step;
+      sum[n] = a[n] = b[n] = 0.0f;
+      if (t >= p.T) continue;
+      b[n] = p.b.p ? p.b.at_far(int64_t(t) * p.b_ts) : 1.0f;
+      if (NEXT) a[n] = p.a.p ? p.a.at_far(int64_t(t) * p.a_ts) : 1.0f;
+      RX::arrived_raw(ring + n * SLOT, lane, at_row<TX>(p.x, t, p.x_ts), c, x_raw[n]);
+      RY::arrived(ring + n * SLOT + E::Y, lane, at_row<TY>(p.y, t, p.y_ts), c, v[n]);
+      P2 yy = 0;
+#pragma unroll
+      for (int j = 0; j < H; ++j) {
+        yy = fma2(v[n][j], v[n][j], yy);
+        v[n][j] = mul2(v[n][j], w[j]);
+      }
+      sum[n] = both(yy);
+      if constexpr (GATED) {
+        P2 g[H], none[H];
+        RY::arrived(ring + n * SLOT + E::GATE, lane, at_row<TY>(p.gate, t, p.gate_ts), c, g);
+        gates<V, false>(p.act, g, none);
+#pragma unroll
+        for (int j = 0; j < H; ++j) v[n][j] = mul2(v[n][j], g[j]);
+      }
+    }
+    slot_read<ODD>();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const uint32_t t = t0 + (N + n) * step;
+      if (t < p.T) copy(t, ring + n * SLOT);
+    }
+    if (p.norm) Sum::run(sum, total, red, turn, G, group, lane, warp);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const uint32_t t = t0 + n * step;
+      const float rho = p.norm ? p.scale * rsqrtf(of_total(total, n) * inv_c + p.eps) : p.scale;
+      sum[n] = 0.0f;
+      if (t >= p.T) continue;
+      TX* out = static_cast<TX*>(p.out) + uint64_t(t) * uint32_t(C);
+      const P2 b2 = twice(b[n] * rho);
+      P2 x[H];
+      RX::values(x_raw[n], x);
+#pragma unroll
+      for (int j = 0; j < H; ++j) v[n][j] = fma2(b2, v[n][j], x[j]);
+      if constexpr (NEXT) {
+        P2 uu = 0;
+        const P2 a2 = twice(a[n]);
+        RX::store_rounded(out, c, lane, C, v[n]);
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+          v[n][j] = mul2(a2, v[n][j]);
+          uu = fma2(v[n][j], v[n][j], uu);
+        }
+        sum[n] = both(uu);
+      } else {
+        RX::store(out, c, lane, C, v[n]);
+      }
+    }
+    if constexpr (NEXT) {
+      Sum::run(sum, total, red_next, turn_next, G, group, lane, warp);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const uint32_t t = t0 + n * step;
+        const P2 r = twice(rsqrtf(of_total(total, n) * inv_c + p.eps_next));
+        if (t >= p.T) continue;
+#pragma unroll
+        for (int j = 0; j < H; ++j) v[n][j] = mul2(v[n][j], mul2(r, wn[j]));
+        RY::store(static_cast<TY*>(p.h) + uint64_t(t) * uint32_t(C), c, lane, C, v[n]);
+      }
+    }
+  }
+  copy_wait_all();
+}
+
 namespace {
+
+template <class TX, class TY, int V, int ODD, bool NEXT, bool GATED>
+bool forward(const Params& p, cudaStream_t s, cudaError_t* e) {
+  using E = ResidualForward<TX, TY, V, ODD, GATED>;
+  const int w = Weights::kind(p.w, NEXT ? p.wn : p.w);
+  if (w == 0 || (w == 2 && ODD) || (p.C + V - 1) / V > kMaxGroup) return false;
+  Params q = p;
+  const Shape sh = plan(q, shape_of(p.T, p.C, V, 1, kMaxGroup), V,
+                        [&](int G, int) { return Need{E::TOKENS * E::SLOT, 0, 4 * E::Sum::floats(G) * (NEXT ? 2 : 1)}; });
+  if (q.direct || items(p.C, V, sh.G) != 1) return false;
+  int grid;
+  *e = w == 1 ? launch<residual_kernel<TX, TY, V, ODD, NEXT, GATED, 1>>(q, sh, 1 << 30, &grid, s)
+              : launch<residual_kernel<TX, TY, V, ODD, NEXT, GATED, ODD ? 1 : 2>>(q, sh, 1 << 30, &grid, s);
+  return true;
+}
+
+template <class TX, class TY, int V, int ODD>
+bool forward(const Params& p, cudaStream_t s, cudaError_t* e) {
+  if (p.h)
+    return p.gate ? forward<TX, TY, V, ODD, true, true>(p, s, e) : forward<TX, TY, V, ODD, true, false>(p, s, e);
+  return p.gate ? forward<TX, TY, V, ODD, false, true>(p, s, e) : forward<TX, TY, V, ODD, false, false>(p, s, e);
+}
 
 template <class TX, class TY, int V, int ODD, bool NEXT, bool GATED>
 bool backward(const Params& p, int* rows, cudaStream_t s, cudaError_t* e) {
@@ -259,6 +418,14 @@ bool backward(const Params& p, int* rows, cudaStream_t s, cudaError_t* e) {
 }
 
 }  // namespace
+
+bool residual_forward(const Params& p, int x_bf16, int y_bf16, bool vec, cudaStream_t s, cudaError_t* e) {
+  if (p.S != 1 || p.P.p != nullptr) return false;
+  if (!vec && y_bf16) return false;
+  if (x_bf16) return forward<bf16_t, bf16_t, 8, 0>(p, s, e);
+  if (y_bf16) return forward<float, bf16_t, 4, 0>(p, s, e);
+  return vec ? forward<float, float, 4, 0>(p, s, e) : forward<float, float, 4, 2>(p, s, e);
+}
 
 bool residual_backward(const Params& p, int x_bf16, int y_bf16, bool vec, int* rows, cudaStream_t s, cudaError_t* e) {
   if (p.S != 1 || p.P.p != nullptr) return false;
