@@ -11,7 +11,8 @@ The residual is S streams of C channels per token, x [..., S, C].
 
 All three are differentiable in every tensor they take.  The gradients are
 also there as functions of their own (enter_backward, leave_backward,
-leave_enter_backward).  x and what is shaped like it is fp32 or bf16; y, h
+leave_enter_backward).  Forward-mode differentiation is refused
+(NotImplementedError).  x and what is shaped like it is fp32 or bf16; y, h
 and the gate are of one type, x's or bf16; coefficients and weights are fp32
 or bf16 each.  Arithmetic is fp32, every result is rounded once.
 """
@@ -21,6 +22,7 @@ import struct
 from collections import namedtuple
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _DT, _lib
@@ -48,7 +50,7 @@ _module = None
 
 def _plain():
     """The extension module for plain arguments (contiguous tensors on the
-    current device): its functions return None where anything else is asked
+    current device, without tangents): its functions return None where anything else is asked
     or is wrong, and the code here does the call in full."""
     global _module
     if _module is None:
@@ -223,6 +225,7 @@ def enter_backward(dh: torch.Tensor, x: torch.Tensor, a: torch.Tensor = None, we
         got = _plain().enter_backward(dh, x, a, weight, eps, dres)
         if got is not None:
             return EnterGrads._make(got)
+    _no_tangent("enter_backward", dh, x, a, weight, dres)
     shape, lead, T, S, C, dev = _x(x)
     if not isinstance(dh, torch.Tensor):
         _wrong(dh, "dh", None, None, None)
@@ -285,6 +288,8 @@ def _leave_backward(dout, dh, out, x, y, P, b, gate, act, weight, norm, scale, e
                                       a_next, weight_next, eps_next)
         if got is not None:
             return got
+    _no_tangent("leave_backward" if dh is None else "leave_enter_backward", dout, dh, out, x, y, P, b, gate, weight, a_next,
+                weight_next)
     shape, lead, T, S, C, dev = _x(x)
     if not isinstance(y, torch.Tensor):
         _wrong(y, "y", None, None, None)
@@ -397,7 +402,22 @@ class _LeaveEnter(torch.autograd.Function):
         return (g.dx, g.dy, g.dP, g.db, g.dgate, g.dweight, g.da_next, g.dweight_next, None, None, None, None, None)
 
 
+def _tangent(tensors):
+    """Whether one of them carries a forward-mode tangent."""
+    return forward_ad._current_level >= 0 and any(
+        isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
+def _no_tangent(name, *tensors):
+    if _tangent(tensors):
+        raise NotImplementedError("%s has no forward-mode derivative" % name)
+
+
 def _learns(*tensors):
+    """Whether the call goes through its autograd function: to record it, or
+    to have a tangent refused (which grad mode has no say in)."""
+    if _tangent(tensors):
+        return True
     if not torch.is_grad_enabled():
         return False
     for t in tensors:

@@ -1,6 +1,6 @@
 // block_binding.cpp -- the Python calls of block.py and optim.py for plain
 // arguments: contiguous CUDA tensors of one device, the current one, with no
-// gradient to record.  A function here checks its tensors, allocates the
+// gradient to record and no forward-mode tangent.  A function here checks its tensors, allocates the
 // results, packs hcb_args and calls the library; where anything is not plain,
 // or the library refuses, it returns None and has done nothing, and the Python
 // code goes through the same call in full (views, errors, other devices).
@@ -45,6 +45,7 @@ struct Call {
   bool fits(const at::Tensor* t) {
     if (t == nullptr || !t->is_cuda() || !t->is_contiguous() || t->layout() != at::kStrided) return plain = false;
     if (t->get_device() != dev) return plain = false;
+    if (t->_fw_grad(/*level=*/0).defined()) return plain = false;  // refused by the Python code, whatever the grad mode
     learns = learns || t->requires_grad();
     return true;
   }
