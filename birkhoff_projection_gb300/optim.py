@@ -37,6 +37,8 @@ class AdamW(torch.optim.Optimizer):
     may set its own lr, betas, eps and weight_decay.  state_bits: 32 or 8.
     master_weights: keep an fp32 copy of bf16 parameters and step on that.
     step(grad_scale=t) multiplies every gradient by the fp32 device scalar t.
+    Autograd knows of a step as of any change in place: a graph that keeps the
+    old parameters is refused by backward.
     A parameter without a gradient is left alone, and so are its moments; all
     parameters share one count of steps (the attribute `steps`).  The count and
     the group's numbers are arguments of the launch: a step captured into a CUDA
@@ -160,12 +162,12 @@ class AdamW(torch.optim.Optimizer):
                                        or grad_scale.device != self._device):
             raise ValueError("grad_scale must be one float32 on %s" % self._device)
         dev = self._device.index
-        calls = []  # the tables, and whatever they point to that is not kept elsewhere
+        calls = []  # the tables, the parameters in them, and whatever they point to that is not kept elsewhere
         plain = binding().adamw_table
         for group, dtype, params, rows, packed in self._plans:
             got = plain(params, packed, _DT[dtype], dev)  # None where the gradients are not all plain
             if got is not None:
-                calls.append((group, _DT[dtype], got[1], got[0], None))
+                calls.append((group, _DT[dtype], got[1], got[0], params, None))
                 continue
             grads = [p.grad for p in params]
             if any([g is None for g in grads]):  # (`in` would compare tensors)
@@ -193,9 +195,10 @@ class AdamW(torch.optim.Optimizer):
                 if len(kinds) > 1:
                     mine = array("Q", [v for k, g in enumerate(grads) if g.dtype == kind
                                        for v in table[k * _FIELDS:(k + 1) * _FIELDS]])
+                    theirs = [p for p, g in zip(params, grads) if g.dtype == kind]
                 else:
-                    mine = table
-                calls.append((group, _DT[dtype], _DT[kind], mine.tobytes(), grads))
+                    mine, theirs = table, params
+                calls.append((group, _DT[dtype], _DT[kind], mine.tobytes(), theirs, grads))
         for group, *_ in calls:  # before the first launch
             self._check(group["lr"], group["betas"], group["eps"], group["weight_decay"])
         scale = 0 if grad_scale is None else grad_scale.data_ptr()
@@ -209,11 +212,14 @@ class AdamW(torch.optim.Optimizer):
 
     def _launch(self, calls, scale):
         f, stream = lib().adamw_step, torch._C._cuda_getCurrentRawStream(self._device.index)
-        for group, p_type, g_type, table, _ in calls:
+        for group, p_type, g_type, table, params, _ in calls:
             beta1, beta2 = group["betas"]
             opts = _OPTS.pack(p_type, g_type, self.state_bits, group["lr"], beta1, beta2, group["eps"],
                               group["weight_decay"], self.steps + 1, scale)
             check(f(table, len(table) // (8 * _FIELDS), opts, stream), "adamw_step")
+            # the kernel writes by address: autograd is told, so that a graph which
+            # keeps the old values is refused
+            torch.autograd.graph.increment_version(params)
 
     _marked_step = staticmethod(torch.optim.Optimizer.profile_hook_step(_step))
 
