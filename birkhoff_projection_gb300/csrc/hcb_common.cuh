@@ -681,6 +681,21 @@ __device__ __forceinline__ float of_total(const float (&total)[CH], int i) {
   return r;
 }
 
+// The sums that enter's gradient takes over a row: <G, x_s>, then <u, x_s>,
+// then <G, u> and <u, u>.  Those are also sum_s a_s <G, x_s> and sum_s a_s
+// <u, x_s>, but where the streams nearly cancel in u that keeps the rounding
+// of the streams' sums: two streams alike to 1/1000 with the coefficients 1 and
+// -0.999 leave <u, u> an error of 1e-4, and 1e-7 summed from u.  Of one stream,
+// u = a x, nothing cancels.
+__host__ __device__ constexpr int next_sums(int SP) { return SP > 1 ? 2 * SP + 2 : 2; }
+template <int SP>
+__device__ __forceinline__ void sums_of_u(const float (&total)[1], float a, float& gu, float& uu) {
+  if constexpr (SP > 1)
+    gu = of_total(total, 2 * SP), uu = of_total(total, 2 * SP + 1);
+  else
+    gu = a * of_total(total, 0), uu = a * of_total(total, 1);
+}
+
 // ---------------------------------------------------------------------------
 // Gates: value and slope of act(g).  e = exp(-|g|) keeps 1 - sigmoid exact
 // to fp32 on both sides and never overflows.

@@ -124,11 +124,11 @@ __global__ void __launch_bounds__(kMaxGroup) enter_kernel(const Params p) {
   copy_wait_all();
 }
 
-// With G = w dh all sums of the gradient are linear in <G, x_s> and <u, x_s>:
-// <G, u> = sum a_s <G, x_s>, <u, u> = sum a_s <u, x_s> and
-// da_s = r (<G, x_s> - k <u, x_s>), so one pass over the row finds them and
-// a second, over what the first kept and over dres, writes.
-// 16384 x 4 x 4096 bf16: 289 us, 6.0 TB/s, 89% of the copy's rate (fp32
+// With G = w dh the gradient needs the sums <G, x_s>, <u, x_s> (for da_s =
+// r (<G, x_s> - k <u, x_s>)), <G, u> and <u, u>; one pass over the row finds
+// them and a second, over what the first kept and over dres, writes.  The last
+// two are summed from u itself (next_sums in hcb_common.cuh).
+// 16384 x 4 x 4096 bf16: 290 us, 6.0 TB/s, 89% of the copy's rate (fp32
 // streams with bf16 rows 95%).  Two slots to a warp and two CTAs on an SM: one
 // slot 322 us, three 305, three CTAs (spilt) 399; half as many threads with
 // two items each 322.
@@ -137,7 +137,7 @@ struct EnterBackward {
   using RX = Row<TX, V, ODD>;
   using RY = Row<TY, V, ODD>;
   using Co = Coefficients<SP, false, false, true>;
-  using Sum = GroupSum<2 * SP>;
+  using Sum = GroupSum<next_sums(SP)>;
   static constexpr int DEPTH = 2;
   // a slot: the streams (or dres), then dh
   static constexpr int DH = SP * RX::SLOT, SLOT = DH + RY::SLOT;
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(256, SP == 8 ? 1 : 2) enter_backward_kernel(co
     Co::read(co_s, Co::NB, a);
     const TX* x = at_row<TX>(p.x, t, p.x_ts);
     const TY* dh = at_row<TY>(p.dh, t, p.dh_ts);
-    P2 sum2[2 * SP] = {};
+    P2 sum2[next_sums(SP)] = {};
     char* item = item0;
 #pragma unroll 1
     for (int c = c0, k = 0; k < K; ++k, c += GV, item += ITEM) {
@@ -261,21 +261,23 @@ __global__ void __launch_bounds__(256, SP == 8 ? 1 : 2) enter_backward_kernel(co
             }
           }
         }
+        if constexpr (SP > 1) {
+#pragma unroll
+          for (int j = 0; j < H; ++j) {
+            sum2[2 * SP] = fma2(g[j], u[j], sum2[2 * SP]);
+            sum2[2 * SP + 1] = fma2(u[j], u[j], sum2[2 * SP + 1]);
+          }
+        }
         keep<V>(item, lane, u);
       }
       copy_next();
       slot = slot == ring + (DEPTH - 1) * E::SLOT ? ring : slot + E::SLOT;
     }
-    float sum[2 * SP], total[1];
+    float sum[next_sums(SP)], total[1], gu, uu;
 #pragma unroll
-    for (int i = 0; i < 2 * SP; ++i) sum[i] = both(sum2[i]);
+    for (int i = 0; i < next_sums(SP); ++i) sum[i] = both(sum2[i]);
     Sum::run(sum, total, red, turn, G, group, lane, warp);
-    float gu = 0.0f, uu = 0.0f;
-#pragma unroll
-    for (int s = 0; s < SP; ++s) {
-      gu += low(a[s]) * of_total(total, s);
-      uu += low(a[s]) * of_total(total, SP + s);
-    }
+    sums_of_u<SP>(total, low(a[0]), gu, uu);
     const float r = rsqrtf(uu * inv_c + p.eps);
     const float k_u = gu * inv_c * r * r;
     if (p.da) {

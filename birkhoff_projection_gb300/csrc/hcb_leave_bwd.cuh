@@ -31,7 +31,7 @@ struct LeaveBackward {
   // dP's sums as pairs of channels, where the registers hold twice as many
   static constexpr bool PAIRS = SP <= 2 || (SP == 4 && V == 4);
   using Sum = GroupSum<R>;
-  using SumNext = GroupSum<2 * SP>;
+  using SumNext = GroupSum<next_sums(SP)>;
   // CTAs that the registers have to leave room for on an SM
   static constexpr int minb(int gate) { return SP == 1 && gate == 0 ? 3 : SP <= 4 ? 2 : 1; }
   // a slot: dout, y, gate and x; or the stored result, and dh where y would be
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
     if constexpr (NEXT) {
       const TX* o = at_row<TX>(p.out_in, t, p.out_ts);
       const TY* dh = at_row<TY>(p.dh, t, p.dh_ts);
-      P2 a[SP], sum2[2 * SP] = {};
+      P2 a[SP], sum2[next_sums(SP)] = {};
       Co::read(co_s, Co::NB, a);
       char *item = item0, *slot = ring;
       if (WHOLE) slots_ready<ODD>();
@@ -177,18 +177,20 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
             }
           }
         }
+        if constexpr (SP > 1) {
+#pragma unroll
+          for (int j = 0; j < H; ++j) {
+            sum2[2 * SP] = fma2(g[j], u[j], sum2[2 * SP]);
+            sum2[2 * SP + 1] = fma2(u[j], u[j], sum2[2 * SP + 1]);
+          }
+        }
         keep<V>(item, lane, u);
       }
-      float sum[2 * SP], total[1];
+      float sum[next_sums(SP)], total[1], gu, uu;
 #pragma unroll
-      for (int i = 0; i < 2 * SP; ++i) sum[i] = both(sum2[i]);
+      for (int i = 0; i < next_sums(SP); ++i) sum[i] = both(sum2[i]);
       E::SumNext::run(sum, total, red_next, turn_next, G, group, lane, warp);
-      float gu = 0.0f, uu = 0.0f;
-#pragma unroll
-      for (int s = 0; s < SP; ++s) {
-        gu += low(a[s]) * of_total(total, s);
-        uu += low(a[s]) * of_total(total, SP + s);
-      }
+      sums_of_u<SP>(total, low(a[0]), gu, uu);
       r_next = rsqrtf(uu * inv_c + p.eps_next);
       k_next = gu * inv_c * r_next * r_next;
       if (p.da) {
