@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(256, Leave<SP, EXACT, TX, TY, V, ODD>::MINB) l
       if (gated) {
         P2 g[H];
         RY::arrived(slot + E::Y + RY::SLOT, lane, gate, c, g);
-        gates<V, false>(p.act, g, w);
+        gates<TY, V, false>(p.act, g, w);
 #pragma unroll
         for (int j = 0; j < H; ++j) v[j] = mul2(v[j], g[j]);
       }

@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
       }
       if (gated) {
         P2 slope[H];
-        gates<V, true>(p.act, g, slope);
+        gates<TY, V, true>(p.act, g, slope);
 #pragma unroll
         for (int j = 0; j < H; ++j) {
           slope[j] = mul2(slope[j], mul2(e[j], dv[j]));

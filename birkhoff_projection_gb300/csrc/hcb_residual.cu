@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) residual_backward_kernel(const P
       if constexpr (GATED) {
         P2 g[H];
         RY::arrived(ring + n * SLOT + E::GATE, lane, at_row<TY>(p.gate, t, p.gate_ts), c, g);
-        gates<V, true>(p.act, g, slope[n]);
+        gates<TY, V, true>(p.act, g, slope[n]);
 #pragma unroll
         for (int j = 0; j < H; ++j) {
           slope[n][j] = mul2(slope[n][j], mul2(e[j], dv[n][j]));
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kMaxGroup, ResidualForward<TX, TY, V, ODD, GAT
       if constexpr (GATED) {
         P2 g[H], none[H];
         RY::arrived(ring + n * SLOT + E::GATE, lane, at_row<TY>(p.gate, t, p.gate_ts), c, g);
-        gates<V, false>(p.act, g, none);
+        gates<TY, V, false>(p.act, g, none);
 #pragma unroll
         for (int j = 0; j < H; ++j) v[n][j] = mul2(v[n][j], g[j]);
       }
