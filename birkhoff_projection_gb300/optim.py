@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import struct
 from array import array
+from collections import defaultdict
 
 import torch
 from torch.optim import optimizer as _hooks
@@ -29,6 +30,10 @@ _FIELDS = 8
 _OPTS = struct.Struct("<3i4x5dqQ")
 
 
+def _bytes(t):
+    return t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t
+
+
 class AdamW(torch.optim.Optimizer):
     """AdamW with decoupled weight decay, one launch for up to 256 tensors of
     a group.
@@ -42,7 +47,8 @@ class AdamW(torch.optim.Optimizer):
     A parameter without a gradient is left alone, and so are its moments; all
     parameters share one count of steps (the attribute `steps`).  The count and
     the group's numbers are arguments of the launch: a step captured into a CUDA
-    graph repeats that very step."""
+    graph repeats that very step.  copy.deepcopy and pickle of the optimizer
+    together with its parameters give one that goes on by itself."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 1e-2, *,
                  state_bits: int = 32, master_weights: bool = False):
@@ -222,6 +228,21 @@ class AdamW(torch.optim.Optimizer):
             torch.autograd.graph.increment_version(params)
 
     _marked_step = staticmethod(torch.optim.Optimizer.profile_hook_step(_step))
+
+    def __getstate__(self):
+        """For copy.deepcopy and pickle, with the parameters.  The state goes
+        as its packed buffers (a parameter's views would each take all of one
+        along), e4m3 numbers as bytes (not every pickle has the type)."""
+        return {**super().__getstate__(), "state": {}, "steps": self.steps, "state_bits": self.state_bits,
+                "master_weights": self.master_weights, "_packed": {k: _bytes(t) for k, t in self._packed.items()}}
+
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        packed, self.state = self._packed, defaultdict(dict)
+        self._pack()
+        for k, t in self._packed.items():
+            _bytes(t).copy_(packed[k])
+        self._ready = True
 
     def state_dict(self):
         d = super().state_dict()
