@@ -12,6 +12,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstring>
@@ -309,7 +310,7 @@ PyObject* adamw_table_impl(PyObject* const* o) {
                        static_cast<Py_ssize_t>(n * sizeof(adamw_tensor)), static_cast<int>(kind));
 }
 
-// Calls IMPL with exactly N arguments; C++ exceptions become Python's.
+// Calls IMPL with exactly N arguments; C++ exceptions become Python's, with the types that torch gives them.
 template <PyObject* (*IMPL)(PyObject* const*), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != N) {
@@ -318,8 +319,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
   try {
     return IMPL(args);
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    torch::translate_exception_to_python(std::current_exception());
     return nullptr;
   }
 }
