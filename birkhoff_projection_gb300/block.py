@@ -42,6 +42,7 @@ LeaveEnterGrads = namedtuple("LeaveEnterGrads", "dx dy dP db dgate dweight da_ne
 # eps_next scale; x y gate P a b w w_next dout dh dres out_in; their strides;
 # h out dx dy dgate dP da db dw dw_next workspace, workspace_bytes
 _ARGS = struct.Struct("<q11i3f12Q14q11QQ")
+_MAX_STRIDE = 2 ** 29 - 1
 _NONE = (None, 0, 0, 0)  # a tensor that is not there: itself, address, type, stride
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _functions = {}
@@ -88,10 +89,12 @@ def _wrong(t, name, shape, dtype, dev):
 
 def _flat(t, inner):
     """t with its leading dimensions as one (a view where their strides allow
-    it), the last dimension contiguous."""
+    it), the last dimension contiguous.  Rows further apart than the library's
+    strides go are copied: they are few (the last tokens of long buffers), or
+    would not fit the GPU."""
     if t.dim() != inner + 1:
         t = t.flatten(0, t.dim() - inner - 1) if t.dim() > inner else t.unsqueeze(0)
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.shape[-1] > 1 and t.stride(-1) != 1 or max(t.stride()) > _MAX_STRIDE:
         t = t.contiguous()
     return t
 

@@ -24,3 +24,21 @@ def test_out_of_memory_is_torchs_own_error():
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert block.enter(x).shape == dh.shape
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_the_last_token_of_a_long_buffer(dtype):
+    """Tokens that are further apart than the library's strides go (2^29)."""
+    L, S, C = 33000, 4, 4096
+    buf = torch.empty(2, L, S, C, dtype=dtype, device=DEV)
+    rows = torch.empty(2, 1 << 29, dtype=dtype, device=DEV)[:, None, :C]
+    assert buf.stride(0) > 1 << 29 and rows.stride(0) == 1 << 29
+    g = torch.Generator().manual_seed(0)
+    buf[:, -1] = torch.randn(2, S, C, generator=g).to(dtype).to(DEV)
+    rows.copy_(torch.randn(2, 1, C, generator=g))
+    x, packed, y = buf[:, -1:], buf[:, -1:].contiguous(), rows.contiguous()
+    assert torch.equal(block.enter(x), block.enter(packed))
+    assert torch.equal(block.leave(x, rows, gate=rows), block.leave(packed, y, gate=y))
+    for p, q in ((block.enter_backward(rows, x, dres=x), block.enter_backward(y, packed, dres=packed)),
+                 (block.leave_enter_backward(x, rows, x, x, rows), block.leave_enter_backward(packed, y, packed, packed, y))):
+        assert all(s is None and t is None or torch.equal(s, t) for s, t in zip(p, q))
