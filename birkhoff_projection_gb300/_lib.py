@@ -145,19 +145,35 @@ def lib():
 _binding = None
 
 
+class _NoBinding:
+    """Stands in for the extension module: no call is one that it takes."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+def _load_binding(handle):
+    loader = importlib.machinery.ExtensionFileLoader("_block_binding", _build.build_binding())
+    spec = importlib.util.spec_from_loader("_block_binding", loader)
+    module = importlib.util.module_from_spec(spec)
+    loader.exec_module(module)
+    module.init(*[ctypes.cast(getattr(handle, name), ctypes.c_void_p).value for name in (
+        "hcb_enter", "hcb_enter_backward", "hcb_leave", "hcb_leave_backward", "hcb_workspace_bytes")])
+    return module
+
+
 def binding():
     """The extension module that makes the plain calls of the block and
-    optimizer entry points (built with the library; loaded on first use)."""
+    optimizer entry points (built and loaded on first use); where it cannot be
+    built or loaded, a stand-in that leaves every call to the Python code."""
     global _binding
     if _binding is None:
         handle = lib()
-        loader = importlib.machinery.ExtensionFileLoader("_block_binding", _build.BINDING_PATH)
-        spec = importlib.util.spec_from_loader("_block_binding", loader)
-        module = importlib.util.module_from_spec(spec)
-        loader.exec_module(module)
-        module.init(*[ctypes.cast(getattr(handle, name), ctypes.c_void_p).value for name in (
-            "hcb_enter", "hcb_enter_backward", "hcb_leave", "hcb_leave_backward", "hcb_workspace_bytes")])
-        _binding = module
+        try:
+            _binding = _load_binding(handle)
+        except (RuntimeError, ImportError) as e:
+            _build.without_binding(e)
+            _binding = _NoBinding()
     return _binding
 
 

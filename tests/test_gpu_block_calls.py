@@ -3,7 +3,7 @@ allocate and what they raise."""
 import pytest
 import torch
 
-from birkhoff_projection_gb300 import block
+from birkhoff_projection_gb300 import _lib, block, optim
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -42,3 +42,21 @@ def test_the_last_token_of_a_long_buffer(dtype):
     for p, q in ((block.enter_backward(rows, x, dres=x), block.enter_backward(y, packed, dres=packed)),
                  (block.leave_enter_backward(x, rows, x, x, rows), block.leave_enter_backward(packed, y, packed, packed, y))):
         assert all(s is None and t is None or torch.equal(s, t) for s, t in zip(p, q))
+
+
+def test_without_the_extension_module(monkeypatch):
+    """Where it cannot be built, the same results come through the Python code."""
+    def results():
+        torch.manual_seed(0)
+        x, y = torch.randn(5, 4, 72, device=DEV), torch.randn(5, 72, device=DEV)
+        w = torch.nn.Parameter(torch.randn(72, device=DEV))
+        opt = optim.AdamW([w], state_bits=8)
+        out, h = block.leave_enter(x, y, weight=w, weight_next=w)
+        (out.sum() + (h * y).sum()).backward()
+        opt.step()
+        return out.detach(), h.detach(), w.grad, w.detach()
+
+    want = results()
+    monkeypatch.setattr(_lib, "_binding", _lib._NoBinding())
+    monkeypatch.setattr(block, "_module", None)
+    assert all(torch.equal(p, q) for p, q in zip(want, results()))
