@@ -1,5 +1,7 @@
 """Calls of the block operators from Python: what they take, what they
 allocate and what they raise."""
+import gc
+
 import pytest
 import torch
 
@@ -11,6 +13,8 @@ DEV = "cuda:0"
 
 def test_out_of_memory_is_torchs_own_error():
     """From the extension module as from torch: what a caller catches to retry with less."""
+    gc.collect()
+    torch.cuda.empty_cache()  # so that these have segments of their own, with no room beside them
     x = torch.zeros(1 << 14, 4, 2048, device=DEV)  # 512 MB, its row 128
     dh = torch.zeros(1 << 14, 2048, device=DEV)
     torch.cuda.synchronize()
