@@ -171,9 +171,9 @@ def _gate(gate, act, shape, dtype, dev):
     return kind, ptr, ts, t
 
 
-def _like(t):
-    """A new contiguous tensor for the gradient of t, and its address."""
-    if t is None:
+def _like(t, wanted=True):
+    """A new contiguous tensor for the gradient of t, if it is wanted, and its address."""
+    if t is None or not wanted:
         return None, 0
     if not isinstance(t, torch.Tensor):
         raise TypeError("expected a torch.Tensor, got %s" % type(t).__name__)
@@ -218,16 +218,14 @@ def _enter(x, a, weight, eps, out_dtype):
     return h
 
 
-def enter_backward(dh: torch.Tensor, x: torch.Tensor, a: torch.Tensor = None, weight: torch.Tensor = None, *,
-                   eps: float = 1e-6, dres: torch.Tensor = None, workspace: torch.Tensor = None) -> EnterGrads:
-    """The gradients of enter: (dx, da, dweight), da and dweight None where
-    a and weight are.  dres, shaped like x, is added to dx: the gradient that
-    the streams have from elsewhere.  workspace: a uint8 tensor of
-    workspace_bytes (allocated here if not given)."""
+_ALL = -1  # every gradient; otherwise bit k stands for the k-th of a function's results
+
+
+def _enter_backward(dh, x, a, weight, eps, dres, workspace, want):
     if workspace is None:
-        got = _plain().enter_backward(dh, x, a, weight, eps, dres)
+        got = _plain().enter_backward(dh, x, a, weight, eps, dres, want)
         if got is not None:
-            return EnterGrads._make(got)
+            return got
     _no_tangent("enter_backward", dh, x, a, weight, dres)
     shape, lead, T, S, C, dev = _x(x)
     if not isinstance(dh, torch.Tensor):
@@ -237,19 +235,28 @@ def enter_backward(dh: torch.Tensor, x: torch.Tensor, a: torch.Tensor = None, we
     rp = r_ts = r_ss = 0
     if dres is not None:
         dres, rp, r_ts, r_ss = _streams(dres, "dres", shape, x.dtype, dev)
-    dx, dxp = _like(x)
-    da, dap = _like(a)
-    dw, dwp = _like(weight)
+    dx, dxp = _like(x, want & 1)
+    da, dap = _like(a, want & 2)
+    dw, dwp = _like(weight, want & 4)
     x, xp, x_ts, x_ss = _streams(x, "x", shape, x.dtype, dev)
     a, ap, ak, a_ts = _few(a, "a", shape[:-1], 1, dev)
     weight, wp, wk, _ = _few(weight, "weight", shape[-1:], 0, dev)
-    workspace, wsp, ws = _scratch(workspace, T, C, weight is not None, x.device)
+    workspace, wsp, ws = _scratch(workspace, T, C, dw is not None, x.device)
     _call("hcb_enter_backward", dev, _ARGS.pack(
         T, S, C, _DT[x.dtype], yk, wk, 0, 0, ak, 0, 0, 1, eps, 0.0, 0.0,
         xp, 0, 0, 0, ap, 0, wp, 0, 0, hp, rp, 0,
         x_ts, x_ss, 0, 0, 0, a_ts, 0, 0, 0, h_ts, r_ts, r_ss, 0, 0,
         0, 0, dxp, 0, 0, 0, dap, 0, dwp, 0, wsp, ws))
-    return EnterGrads(dx, da, dw)
+    return dx, da, dw
+
+
+def enter_backward(dh: torch.Tensor, x: torch.Tensor, a: torch.Tensor = None, weight: torch.Tensor = None, *,
+                   eps: float = 1e-6, dres: torch.Tensor = None, workspace: torch.Tensor = None) -> EnterGrads:
+    """The gradients of enter: (dx, da, dweight), da and dweight None where
+    a and weight are.  dres, shaped like x, is added to dx: the gradient that
+    the streams have from elsewhere.  workspace: a uint8 tensor of
+    workspace_bytes (allocated here if not given)."""
+    return EnterGrads._make(_enter_backward(dh, x, a, weight, eps, dres, workspace, _ALL))
 
 
 def _leave(x, y, P, b, gate, act, weight, norm, scale, eps, want_h, a_next, weight_next, eps_next):
@@ -285,10 +292,10 @@ def _leave(x, y, P, b, gate, act, weight, norm, scale, eps, want_h, a_next, weig
 
 
 def _leave_backward(dout, dh, out, x, y, P, b, gate, act, weight, norm, scale, eps, a_next, weight_next, eps_next,
-                    workspace):
+                    workspace, want=_ALL):
     if workspace is None:
         got = _plain().leave_backward(x, y, P, b, gate, _ACT.get(act, -1), weight, norm, scale, eps, dout, dh, out,
-                                      a_next, weight_next, eps_next)
+                                      a_next, weight_next, eps_next, want)
         if got is not None:
             return got
     _no_tangent("leave_backward" if dh is None else "leave_enter_backward", dout, dh, out, x, y, P, b, gate, weight, a_next,
@@ -299,12 +306,12 @@ def _leave_backward(dout, dh, out, x, y, P, b, gate, act, weight, norm, scale, e
     xt, yt, row = x.dtype, y.dtype, torch.Size((*lead, C))
     yk = _y_type(yt, x, "y")
     # without a mixing matrix dx is dout, unless h's gradient is added to it
-    dx, dxp = _like(x) if P is not None or dh is not None else (dout, 0)
-    dy, dyp = _like(y)
-    dP, dPp = _like(P)
-    db, dbp = _like(b)
-    dgate, dgp = _like(gate)
-    dw, dwp = _like(weight)
+    dx, dxp = _like(x, want & 1 or dh is not None) if P is not None or dh is not None else (dout, 0)
+    dy, dyp = _like(y, want & 2)
+    dP, dPp = _like(P, want & 4)
+    db, dbp = _like(b, want & 8)
+    dgate, dgp = _like(gate, want & 16)
+    dw, dwp = _like(weight, want & 32)
     dout, dop, do_ts, do_ss = _streams(dout, "dout", shape, xt, dev)
     y, yp, y_ts = _row(y, "y", row, yt, dev)
     act, gp, g_ts, gate = _gate(gate, act, row, yt, dev)
@@ -319,8 +326,8 @@ def _leave_backward(dout, dh, out, x, y, P, b, gate, act, weight, norm, scale, e
     if dh is not None:
         dh, hp, h_ts = _row(dh, "dh", row, yt, dev)
         out, op, o_ts, o_ss = _streams(out, "out", shape, xt, dev)
-        da, dap = _like(a_next)
-        dwn, dwnp = _like(weight_next)
+        da, dap = _like(a_next, want & 64)
+        dwn, dwnp = _like(weight_next, want & 128)
         a_next, ap, ak, a_ts = _few(a_next, "a_next", shape[:-1], 1, dev)
         weight_next, wnp, wnk, _ = _few(weight_next, "weight_next", shape[-1:], 0, dev)
     workspace, wsp, ws = _scratch(workspace, T, C, (dw is not None) + (dwn is not None), x.device)
@@ -354,6 +361,11 @@ def leave_enter_backward(dout: torch.Tensor, dh: torch.Tensor, out: torch.Tensor
                                                  weight_next, eps_next, workspace))
 
 
+def _bits(needed):
+    """Which gradients autograd asks for, as `want` has them."""
+    return sum(1 << k for k, n in enumerate(needed) if n)
+
+
 class _Enter(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, a, weight, eps, out_dtype):
@@ -365,7 +377,7 @@ class _Enter(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dh):
         x, a, weight = ctx.saved_tensors
-        return (*enter_backward(dh, x, a, weight, eps=ctx.eps), None, None)
+        return (*_enter_backward(dh, x, a, weight, ctx.eps, None, None, _bits(ctx.needs_input_grad)), None, None)
 
 
 class _Leave(torch.autograd.Function):
@@ -381,8 +393,9 @@ class _Leave(torch.autograd.Function):
     def backward(ctx, dout):
         x, y, P, b, gate, weight = ctx.saved_tensors
         act, norm, scale, eps = ctx.how
-        g = leave_backward(dout, dout if x is None else x, y, P, b, gate=gate, act=act, weight=weight, norm=norm, scale=scale, eps=eps)
-        return (g.dx, g.dy, g.dP, g.db, g.dgate, g.dweight, None, None, None, None)
+        g = _leave_backward(dout, None, None, dout if x is None else x, y, P, b, gate, act, weight, norm, scale, eps, None, None,
+                            0.0, None, _bits(ctx.needs_input_grad))
+        return (*g[:6], None, None, None, None)
 
 
 class _LeaveEnter(torch.autograd.Function):
@@ -393,6 +406,7 @@ class _LeaveEnter(torch.autograd.Function):
         # without a mixing matrix the gradients do not need x's values
         ctx.save_for_backward(None if P is None else x, y, P, b, gate, weight, a_next, weight_next, out)
         ctx.how = how
+        ctx.set_materialize_grads(False)
         return out, h
 
     @staticmethod
@@ -400,9 +414,15 @@ class _LeaveEnter(torch.autograd.Function):
     def backward(ctx, dout, dh):
         x, y, P, b, gate, weight, a_next, weight_next, out = ctx.saved_tensors
         act, norm, scale, eps, eps_next = ctx.how
-        g = leave_enter_backward(dout, dh, out, out if x is None else x, y, P, b, gate=gate, act=act, weight=weight, norm=norm, scale=scale,
-                                 eps=eps, a_next=a_next, weight_next=weight_next, eps_next=eps_next)
-        return (g.dx, g.dy, g.dP, g.db, g.dgate, g.dweight, g.da_next, g.dweight_next, None, None, None, None, None)
+        # results that the loss does not have: without h's gradient it is leave's,
+        # and a zero for that of the streams is one row, repeated
+        if dout is None and dh is None:
+            return (None,) * 13
+        if dout is None:
+            dout = torch.zeros(out.shape[-1], dtype=out.dtype, device=out.device).expand(out.shape)
+        g = _leave_backward(dout, dh, out, out if x is None else x, y, P, b, gate, act, weight, norm, scale, eps, a_next,
+                            weight_next, eps_next, None, _bits(ctx.needs_input_grad))
+        return (*g, None, None, None, None, None)
 
 
 def _tangent(tensors):

@@ -137,8 +137,8 @@ struct Call {
     *at = t.data_ptr();
     return t;
   }
-  at::Tensor like(PyObject* o, void** at) const {
-    if (o == Py_None) return {};
+  at::Tensor like(PyObject* o, void** at, bool wanted = true) const {
+    if (o == Py_None || !wanted) return {};
     const at::Tensor& t = THPVariable_Unpack(o);
     return make(t.sizes(), t.scalar_type(), at);
   }
@@ -180,9 +180,16 @@ bool number(PyObject* o, float* v) {
   return true;
 }
 long whole(PyObject* o) { return PyLong_CheckExact(o) ? PyLong_AsLong(o) : -1; }
+// Which of a gradient's results are wanted, from the argument behind the
+// first n if there is one: bit k stands for result k.
+struct Wanted {
+  unsigned long bits;
+  Wanted(PyObject* const* o, Py_ssize_t n, Py_ssize_t given) : bits(given > n ? whole(o[n]) : ~0ul) {}
+  bool operator[](int k) const { return bits >> k & 1; }
+};
 
 // enter(x, a, weight, eps, y type or -1) -> h
-PyObject* enter_impl(PyObject* const* o) {
+PyObject* enter_impl(PyObject* const* o, Py_ssize_t) {
   Call c(o[0]);
   if (!c.plain || !number(o[3], &c.args.eps)) Py_RETURN_NONE;
   const long type = whole(o[4]);
@@ -198,8 +205,9 @@ PyObject* enter_impl(PyObject* const* o) {
   return wrapped(std::move(h));
 }
 
-// enter_backward(dh, x, a, weight, eps, dres) -> (dx, da, dweight)
-PyObject* enter_backward_impl(PyObject* const* o) {
+// enter_backward(dh, x, a, weight, eps, dres[, wanted]) -> (dx, da, dweight)
+PyObject* enter_backward_impl(PyObject* const* o, Py_ssize_t n) {
+  const Wanted want(o, 6, n);
   Call c(o[1]);
   if (!c.plain || !number(o[4], &c.args.eps)) Py_RETURN_NONE;
   c.streams(o[1], &c.args.x, &c.args.x_ts, &c.args.x_ss);
@@ -208,8 +216,9 @@ PyObject* enter_backward_impl(PyObject* const* o) {
   c.weight(o[3], &c.args.w, &c.args.w_dtype);
   if (o[5] != Py_None) c.streams(o[5], &c.args.dres, &c.args.dres_ts, &c.args.dres_ss);
   if (!c.plain) Py_RETURN_NONE;
-  at::Tensor out[3] = {c.like(o[1], &c.args.dx), c.like(o[2], &c.args.da), c.like(o[3], &c.args.dw)};
-  const at::Tensor ws = c.scratch(o[3] != Py_None);
+  at::Tensor out[3] = {c.like(o[1], &c.args.dx, want[0]), c.like(o[2], &c.args.da, want[1]),
+                       c.like(o[3], &c.args.dw, want[2])};
+  const at::Tensor ws = c.scratch(c.args.dw != nullptr);
   if (!c.run(f_enter_backward)) Py_RETURN_NONE;
   return tuple(out);
 }
@@ -233,7 +242,7 @@ bool leave_inputs(Call& c, PyObject* const* o) {
 }
 
 // leave(x, y, P, b, gate, act, weight, norm, scale, eps, want_h, a_next, weight_next, eps_next) -> (out, h)
-PyObject* leave_impl(PyObject* const* o) {
+PyObject* leave_impl(PyObject* const* o, Py_ssize_t) {
   Call c(o[0]);
   if (!leave_inputs(c, o) || !number(o[13], &c.args.eps_next)) Py_RETURN_NONE;
   c.streams(o[0], &c.args.x, &c.args.x_ts, &c.args.x_ss);
@@ -249,9 +258,10 @@ PyObject* leave_impl(PyObject* const* o) {
   return tuple(out);
 }
 
-// leave_backward(x, y, P, b, gate, act, weight, norm, scale, eps, dout, dh, out, a_next, weight_next, eps_next)
-// -> (dx, dy, dP, db, dgate, dweight, da_next, dweight_next); dh None: leave's alone
-PyObject* leave_backward_impl(PyObject* const* o) {
+// leave_backward(x, y, P, b, gate, act, weight, norm, scale, eps, dout, dh, out, a_next, weight_next, eps_next[, wanted])
+// -> (dx, dy, dP, db, dgate, dweight, da_next, dweight_next); dh None: leave's alone, and otherwise always dx
+PyObject* leave_backward_impl(PyObject* const* o, Py_ssize_t n) {
+  const Wanted want(o, 16, n);
   Call c(o[0]);
   if (!leave_inputs(c, o) || !number(o[15], &c.args.eps_next)) Py_RETURN_NONE;
   const bool mix = o[2] != Py_None, next = o[11] != Py_None;
@@ -266,24 +276,24 @@ PyObject* leave_backward_impl(PyObject* const* o) {
   if (!c.plain) Py_RETURN_NONE;
   at::Tensor out[8];
   // without a mixing matrix dx is dout, unless h's gradient is added to it
-  out[0] = mix || next ? c.like(o[0], &c.args.dx) : THPVariable_Unpack(o[10]);
-  out[1] = c.like(o[1], &c.args.dy);
-  out[2] = c.like(o[2], &c.args.dP);
-  out[3] = c.like(o[3], &c.args.db);
-  out[4] = c.like(o[4], &c.args.dgate);
-  out[5] = c.like(o[6], &c.args.dw);
+  out[0] = mix || next ? c.like(o[0], &c.args.dx, next || want[0]) : THPVariable_Unpack(o[10]);
+  out[1] = c.like(o[1], &c.args.dy, want[1]);
+  out[2] = c.like(o[2], &c.args.dP, want[2]);
+  out[3] = c.like(o[3], &c.args.db, want[3]);
+  out[4] = c.like(o[4], &c.args.dgate, want[4]);
+  out[5] = c.like(o[6], &c.args.dw, want[5]);
   if (next) {
-    out[6] = c.like(o[13], &c.args.da);
-    out[7] = c.like(o[14], &c.args.dw_next);
+    out[6] = c.like(o[13], &c.args.da, want[6]);
+    out[7] = c.like(o[14], &c.args.dw_next, want[7]);
   }
-  const at::Tensor ws = c.scratch((o[6] != Py_None) + (next && o[14] != Py_None));
+  const at::Tensor ws = c.scratch((c.args.dw != nullptr) + (c.args.dw_next != nullptr));
   if (!c.run(f_leave_backward)) Py_RETURN_NONE;
   return tuple(out);
 }
 
 // adamw_table(params, table, p type, device) -> (table, g type): the table is
 // that of adamw_tensor with the addresses of p and g open.
-PyObject* adamw_table_impl(PyObject* const* o) {
+PyObject* adamw_table_impl(PyObject* const* o, Py_ssize_t) {
   if (!PyList_CheckExact(o[0]) || !PyBytes_CheckExact(o[1])) Py_RETURN_NONE;
   const Py_ssize_t n = PyList_GET_SIZE(o[0]);
   const long type = whole(o[2]), dev = whole(o[3]);
@@ -310,15 +320,15 @@ PyObject* adamw_table_impl(PyObject* const* o) {
                        static_cast<Py_ssize_t>(n * sizeof(adamw_tensor)), static_cast<int>(kind));
 }
 
-// Calls IMPL with exactly N arguments; C++ exceptions become Python's, with the types that torch gives them.
-template <PyObject* (*IMPL)(PyObject* const*), Py_ssize_t N>
+// Calls IMPL with N arguments, or up to MORE more; C++ exceptions become Python's, with the types that torch gives them.
+template <PyObject* (*IMPL)(PyObject* const*, Py_ssize_t), Py_ssize_t N, Py_ssize_t MORE = 0>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  if (n != N) {
+  if (n < N || n > N + MORE) {
     PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", N, n);
     return nullptr;
   }
   try {
-    return IMPL(args);
+    return IMPL(args, n);
   } catch (...) {
     torch::translate_exception_to_python(std::current_exception());
     return nullptr;
@@ -351,9 +361,9 @@ PyObject* init(PyObject*, PyObject* const* args, Py_ssize_t n) {
 PyMethodDef methods[] = {
     {"init", FAST(init)},
     {"enter", FAST((entry<enter_impl, 5>))},
-    {"enter_backward", FAST((entry<enter_backward_impl, 6>))},
+    {"enter_backward", FAST((entry<enter_backward_impl, 6, 1>))},
     {"leave", FAST((entry<leave_impl, 14>))},
-    {"leave_backward", FAST((entry<leave_backward_impl, 16>))},
+    {"leave_backward", FAST((entry<leave_backward_impl, 16, 1>))},
     {"adamw_table", FAST((entry<adamw_table_impl, 4>))},
     {nullptr, nullptr, 0, nullptr},
 };
