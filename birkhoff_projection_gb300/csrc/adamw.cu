@@ -18,8 +18,6 @@
 // 599, five 769).
 #include <cuda_runtime.h>
 
-#include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -373,7 +371,7 @@ extern "C" int adamw_step(const adamw_tensor* x, int32_t count, const adamw_opts
   const int pb = o->p_dtype == B4_F32 ? 4 : 2, gb = o->g_dtype == B4_F32 ? 4 : 2;
   bool master = false;
   for (int32_t k = 0; k < count; ++k) {
-    if (x[k].n < 0) return B4_EINVAL;
+    if (x[k].n < 0 || x[k].n > ADAMW_MAX_ELEMENTS) return B4_EINVAL;
     if (k == 0)
       master = x[k].master != nullptr;
     else if (master != (x[k].master != nullptr))
@@ -385,7 +383,6 @@ extern "C" int adamw_step(const adamw_tensor* x, int32_t count, const adamw_opts
     if (eight && (x[k].m_scale == nullptr || x[k].v_scale == nullptr || !placed(x[k].m_scale, 4) ||
                   !placed(x[k].v_scale, 4)))
       return B4_EINVAL;
-    if (x[k].n > (int64_t(1) << 40)) return B4_EINVAL;
   }
   if (master && o->p_dtype == B4_F32) return B4_ENOTIMPL;
 
@@ -405,31 +402,23 @@ extern "C" int adamw_step(const adamw_tensor* x, int32_t count, const adamw_opts
   tab.count = 0;
   for (int32_t k = 0; k < count; ++k) {
     if (x[k].n == 0) continue;
-    // a tensor of more chunks than a grid holds is taken in pieces
-    constexpr int64_t kMost = (int64_t(1) << 30) * kChunk;
-    for (int64_t at = 0; at < x[k].n; at += kMost) {
-      const int64_t n = std::min(x[k].n - at, kMost);
-      const uint32_t chunks = static_cast<uint32_t>((n + kChunk - 1) / kChunk);
-      if (tab.count == kTable || (tab.count > 0 && uint64_t(tab.first[tab.count]) + chunks > 0x7fffffffu)) {
-        const cudaError_t e = launch_any(tab, h, o, master, s);
-        if (e != cudaSuccess) return b4::record_cuda_error(e);
-        tab.count = 0;
-      }
-      const int c = tab.count++;
-      Entry& q = tab.at[c];
-      q.p = static_cast<char*>(x[k].p) + at * pb;
-      q.g = static_cast<const char*>(x[k].g) + at * gb;
-      q.m = static_cast<char*>(x[k].m) + at * (eight ? 1 : 4);
-      q.v = static_cast<char*>(x[k].v) + at * (eight ? 1 : 4);
-      q.m_scale = eight ? x[k].m_scale + at / ADAMW_BLOCK : nullptr;
-      q.v_scale = eight ? x[k].v_scale + at / ADAMW_BLOCK : nullptr;
-      q.master = master ? x[k].master + at : nullptr;
-      q.n = n;
-      q.vec = placed(q.p, 16) && placed(q.g, 16) && placed(q.m, eight ? 8 : 16) && placed(q.v, eight ? 8 : 16) &&
-              placed(q.master, 16);
-      if (c == 0) tab.first[0] = 0;
-      tab.first[c + 1] = tab.first[c] + chunks;
+    const uint32_t chunks = static_cast<uint32_t>((x[k].n + kChunk - 1) / kChunk);  // 2^28 at most
+    if (tab.count == kTable || (tab.count > 0 && uint64_t(tab.first[tab.count]) + chunks > 0x7fffffffu)) {
+      const cudaError_t e = launch_any(tab, h, o, master, s);
+      if (e != cudaSuccess) return b4::record_cuda_error(e);
+      tab.count = 0;
     }
+    const int c = tab.count++;
+    Entry& q = tab.at[c];
+    q.p = x[k].p, q.g = x[k].g, q.m = x[k].m, q.v = x[k].v;
+    q.m_scale = eight ? x[k].m_scale : nullptr;
+    q.v_scale = eight ? x[k].v_scale : nullptr;
+    q.master = x[k].master;
+    q.n = x[k].n;
+    q.vec = placed(q.p, 16) && placed(q.g, 16) && placed(q.m, eight ? 8 : 16) && placed(q.v, eight ? 8 : 16) &&
+            placed(q.master, 16);
+    if (c == 0) tab.first[0] = 0;
+    tab.first[c + 1] = tab.first[c] + chunks;
   }
   if (tab.count == 0) return B4_OK;
   return b4::record_cuda_error(launch_any(tab, h, o, master, s));

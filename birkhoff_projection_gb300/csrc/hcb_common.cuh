@@ -3,7 +3,7 @@
 // shared memory ahead of their use, the sums over a row, gates, and the
 // launch shape.
 //
-// Mapping.  A group of G threads (a power of two, a warp at least) takes one
+// Mapping.  A group of G threads (whole warps, 16 at most) takes one
 // token at a time; a CTA holds NG groups, and the grid is persistent (SMs x
 // resident CTAs).  A warp owns the same blocks of 32 V channels of every
 // token, k = 0 .. K - 1, where V elements are 16 bytes of the wider row type.
@@ -874,10 +874,6 @@ cudaError_t by_streams(int S, int x_bf16, int y_bf16, bool vec, F&& f) {
     default: return by_type<8, false>(x_bf16, y_bf16, vec, f);
   }
 }
-
-// Sum the partial weight gradients [rows, C] and write them (hcb_api.cu).
-cudaError_t finish_weights(const float* part, const float* part_next, int rows, int C, void* dw,
-                           int dw_bf16, void* dwn, int dwn_bf16, cudaStream_t s);
 
 // The pass launchers, one translation unit each: enqueue on `s`.
 cudaError_t enter_forward(const Params& p, int x_bf16, int y_bf16, bool vec, cudaStream_t s);

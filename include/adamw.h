@@ -31,7 +31,7 @@
  * element type is taken; tensors on 16-byte boundaries are fastest.
  *
  * Errors (return values, from birkhoff4.h): B4_EINVAL for a NULL pointer with
- * work to do, a negative count, an unknown type, state_bits or hyperparameter
+ * work to do, a negative count, n outside 0..ADAMW_MAX_ELEMENTS, an unknown type, state_bits or hyperparameter
  * outside its range (beta1, beta2 in [0, 1), eps >= 0, lr and weight_decay
  * finite and >= 0, step >= 1), a pointer that is not aligned to its element;
  * B4_ENOTIMPL for master weights beside fp32 weights; B4_ECUDA for a launch
@@ -53,6 +53,7 @@ extern "C" {
 #endif
 
 #define ADAMW_BLOCK 128
+#define ADAMW_MAX_ELEMENTS (INT64_C(1) << 40) /* of one tensor */
 
 typedef struct {
   void *p;        /* weights [n] */
