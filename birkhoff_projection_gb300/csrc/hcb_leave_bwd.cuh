@@ -20,7 +20,10 @@ namespace hcb {
 // the shared memory of deeper rings; four items to a thread instead of two
 // take 415 us.
 // NEXT adds a run of items before it: D_i = dout_i + a_i du with du from dh,
-// as in enter_backward_kernel.
+// as in enter_backward_kernel.  With what that keeps, four bf16 streams and a
+// gate ask for 129 KB to a CTA of 256 threads, and an SM has one: 16384 x 4 x
+// 4096 741 us, 56% of the copy's rate (enter's and leave's gradients apart 670);
+// without a gate 478 us, 79%.
 template <int SP, class TX, class TY, int V, int ODD, bool NEXT>
 struct LeaveBackward {
   using RX = Row<TX, V, ODD>;

@@ -41,8 +41,8 @@
  *
  * Optional pointers (NULL): a (all ones), P (identity), b (all ones), gate
  * (act = HCB_ACT_NONE), w and w_next (ones), dres (zero); and any gradient
- * that is not wanted.  leave's backward with P == NULL has dx == dout: dx is
- * only written if it is given.
+ * that is not wanted, but dx with dres or with dh.  leave's backward with P ==
+ * NULL and without dh has dx == dout: dx is only written if it is given.
  *
  * Errors (return values, from birkhoff4.h): B4_EINVAL for a NULL pointer with
  * work to do, T outside 0..2^31 - 1, S outside 1..8, C outside
