@@ -9,28 +9,29 @@ namespace hcb {
 
 // Every sum that the gradient needs is linear in what is read, up to the
 // factor rho of y's norm: with q = act(gate) and e = w q y,
-//   dP_ij = <D_i, x_j>,  db_i = scale rho <D_i, e>,
-//   <g, y> = scale sum_i b_i <D_i, e>
-// so one pass over the row finds S^2 + S + 1 sums and writes dx.  It keeps
-// q dv and act'(gate) w y dv (dv = sum_i b_i D_i), of which a second one
-// writes dy, dgate and the weight's shares.
-// 16384 x 4 x 4096 bf16 with a gate: 382 us, 5.6 TB/s, 83% of the copy's rate;
-// 4096 x 4 x 4096 fp32 with bf16 rows: 149 us, 93%.  The 21 sums to a thread
+//   dP_ij = <D_i, x_j>,  db_i = scale rho <D_i, e>,  <g, y> = scale <dv, e>
+// with dv = sum_i b_i D_i, so one pass over the row finds S^2 + S + 2 sums and
+// writes dx.  It keeps q dv and act'(gate) w y dv, of which a second one
+// writes dy, dgate and the weight's shares.  <dv, e> is also sum_i b_i <D_i, e>,
+// but where the D_i nearly cancel in dv that would keep the rounding of the
+// larger sums (next_sums in hcb_common.cuh).
+// 16384 x 4 x 4096 bf16 with a gate: 374 us, 5.8 TB/s, 85% of the copy's rate;
+// 4096 x 4 x 4096 fp32 with bf16 rows: 149 us, 93%.  The 22 sums to a thread
 // take the registers of all but two CTAs of 256 threads, and the shares of dw
 // the shared memory of deeper rings; four items to a thread instead of two
 // take 415 us.
 // NEXT adds a run of items before it: D_i = dout_i + a_i du with du from dh,
 // as in enter_backward_kernel.  With what that keeps, four bf16 streams and a
 // gate ask for 129 KB to a CTA of 256 threads, and an SM has one: 16384 x 4 x
-// 4096 741 us, 56% of the copy's rate (enter's and leave's gradients apart 670);
-// without a gate 478 us, 79%.
+// 4096 758 us, 55% of the copy's rate (enter's and leave's gradients apart 665);
+// without a gate 482 us, 78%.
 template <int SP, class TX, class TY, int V, int ODD, bool NEXT>
 struct LeaveBackward {
   using RX = Row<TX, V, ODD>;
   using RY = Row<TY, V, ODD>;
   using Co = Coefficients<SP, true, true, NEXT, true>;
-  // the sums: dP (by column), <D_i, e>, <y, y>
-  static constexpr int R = SP * SP + SP + 1;
+  // the sums: dP (by column), <D_i, e>, <y, y>, and of several streams <dv, e>
+  static constexpr int YY = SP * SP + SP, DV = YY + 1, R = SP > 1 ? DV + 1 : DV;
   // dP's sums as pairs of channels, where the registers hold twice as many
   static constexpr bool PAIRS = SP <= 2 || (SP == 4 && V == 4);
   using Sum = GroupSum<R>;
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
     const TX* x = at_row<TX>(p.x, t, p.x_ts);
     const TY* y = at_row<TY>(p.y, t, p.y_ts);
     const TY* gate = at_row<TY>(p.gate, t, p.gate_ts);
-    P2 sum_dP2[E::PAIRS ? SP * SP : 1] = {}, sum_e2[SP] = {}, sum_y2 = 0;
+    P2 sum_dP2[E::PAIRS ? SP * SP : 1] = {}, sum_e2[SP] = {}, sum_y2 = 0, sum_dv2 = 0;
     float sum_dP[E::PAIRS ? 1 : SP * SP] = {};
     TX* dx = p.dx ? static_cast<TX*>(p.dx) + uint64_t(t) * uint32_t(S * C) : nullptr;
     char *item = item0, *slot = ring;
@@ -322,9 +323,13 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
         for (int j = 0; j < H; ++j) {
           slope[j] = mul2(slope[j], mul2(e[j], dv[j]));
           e[j] = mul2(e[j], g[j]);
+          if (SP > 1) sum_dv2 = fma2(dv[j], e[j], sum_dv2);
           dv[j] = mul2(dv[j], g[j]);
         }
         keep<V>(item + KB, lane, slope);
+      } else if (SP > 1) {
+#pragma unroll
+        for (int j = 0; j < H; ++j) sum_dv2 = fma2(dv[j], e[j], sum_dv2);
       }
       keep<V>(item, lane, dv);
 #pragma unroll
@@ -337,15 +342,17 @@ __global__ void __launch_bounds__(256, LeaveBackward<SP, TX, TY, V, ODD, NEXT>::
     for (int i = 0; i < SP * SP; ++i) sum[i] = E::PAIRS ? both(sum_dP2[E::PAIRS ? i : 0]) : sum_dP[E::PAIRS ? 0 : i];
 #pragma unroll
     for (int i = 0; i < SP; ++i) sum[SP * SP + i] = both(sum_e2[i]);
-    sum[SP * SP + SP] = both(sum_y2);
+    sum[E::YY] = both(sum_y2);
+    if constexpr (SP > 1) sum[E::DV] = both(sum_dv2);
     Sum::run(sum, total, red, turn, G, group, lane, warp);
-    const float rho = p.norm ? rsqrtf(of_total(total, SP * SP + SP) * inv_c + p.eps) : 1.0f;
-    float gy = 0.0f;
-    {
-      P2 b[SP];
+    const float rho = p.norm ? rsqrtf(of_total(total, E::YY) * inv_c + p.eps) : 1.0f;
+    float gy;
+    if constexpr (SP > 1) {
+      gy = of_total(total, E::DV);
+    } else {
+      P2 b[1];
       Co::read(co_s, Co::NP, b);
-#pragma unroll
-      for (int i = 0; i < SP; ++i) gy += low(b[i]) * of_total(total, SP * SP + i);
+      gy = low(b[0]) * of_total(total, SP * SP);
     }
     const float sr = p.scale * rho;
     const P2 sr2 = twice(sr), minus_k = twice(p.norm ? -sr * gy * inv_c * rho * rho : 0.0f);

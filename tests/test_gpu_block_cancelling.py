@@ -17,6 +17,7 @@ import pytest
 import torch
 
 from birkhoff_projection_gb300 import block
+from oracle.block import gate_value
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -92,3 +93,34 @@ def test_leave_enter(mix, T, S, C, tx, ty, along):
     want = gradients(np64(dh), np64(out), np64(a), np64(w), 1e-12)
     for name, t in (("dx", got.dx), ("da", got.da_next), ("dw", got.dweight_next)):
         close(t, *want[name], name)
+
+
+@pytest.mark.parametrize("tx,ty", [(F, F), (H, H), (F, H)])
+@pytest.mark.parametrize("along", [False, True])
+@pytest.mark.parametrize("T,S,C", SIZES)
+@pytest.mark.parametrize("act,mix,enters", [(None, True, False), ("sigmoid", True, False), (None, False, False), ("silu", True, True)])
+def test_leave(act, mix, enters, T, S, C, tx, ty, along):
+    """The streams' gradients nearly cancel in dv = sum_i b_i D_i, of which
+    <w act dv, y> is a sum: dy.  along: y is along dv, the norm takes that share out."""
+    D, b, w, y = make(T, S, C, tx, ty, along)
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(T, S, C, generator=g).to(tx).to(DEV)
+    gate = None if act is None else torch.randn(T, C, generator=g).to(ty).to(DEV)
+    P = torch.eye(S, device=DEV).expand(T, S, S) if mix else None
+    how = dict(gate=gate, act=act or "sigmoid", weight=w, scale=0.5, eps=1e-12)
+    if enters:  # and with no gradient through the next block's input
+        got = block.leave_enter_backward(D, torch.zeros_like(y), x, x, y, P, b, weight_next=w, **how)
+    else:
+        got = block.leave_backward(D, x, y, P, b, **how)
+    d, n, q, slope = np64(D), np64(y), 1.0, None
+    dv = np.einsum("ts,tsc->tc", np64(b), d)
+    rho = 1 / np.sqrt((n * n).mean(1, keepdims=True) + 1e-12)
+    if act is not None:
+        q, slope, slm = gate_value(act, np64(gate))
+        z = n * rho * np64(w)
+        close(got.dgate, 0.5 * dv * slope * z, 0.5 * np.abs(dv * z) * slm, "dgate")
+    G = 0.5 * q * dv * np64(w)
+    k, km = (G * n).mean(1, keepdims=True) * rho ** 2, np.abs(G * n).mean(1, keepdims=True) * rho ** 2
+    close(got.dy, rho * (G - k * n), rho * (np.abs(G) + km * np.abs(n)), "dy")
+    dz = 0.5 * q * dv * n * rho
+    close(got.dweight, dz.sum(0), np.abs(dz).sum(0), "dweight")
